@@ -26,7 +26,8 @@ import torch
 from . import _abi
 
 __all__ = ["chunk_kda", "chunk_kda_bwd", "fused_recurrent_kda", "gate_chunk_cumsum", "KDAContractError", "KDARuntimeError",
-           "workspace_bytes", "library"]
+           "workspace_bytes", "library", "short_conv", "short_conv_bwd", "short_conv_step", "rms_norm", "rms_norm_fp8",
+           "rms_norm_bwd"]
 
 
 class KDAContractError(ValueError):
@@ -447,3 +448,7 @@ def gate_chunk_cumsum(g: torch.Tensor, *, chunk_size: int = 64, use_gate_in_kern
     if rc != _abi.KDA_OK:
         _raise(rc, lib)
     return g_act, g_cum
+
+
+from .layers import (rms_norm, rms_norm_bwd, rms_norm_fp8, short_conv, short_conv_bwd,  # noqa: E402
+                     short_conv_step)

@@ -36,6 +36,8 @@ EXPORTS = (
     "kda_chunk_bwd_workspace_size", "kda_chunk_bwd", "kda_chunk_fwd_noalloc",
     "kda_chunk_bwd_tokenwise_workspace_size", "kda_chunk_bwd_tokenwise", "kda_chunk_fwd_save",
     "kda_chunk_bwd_saved",
+    "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_size", "kda_short_conv_bwd", "kda_short_conv_step",
+    "kda_rms_norm_fwd", "kda_rms_norm_fp8", "kda_rms_norm_bwd_workspace_size", "kda_rms_norm_bwd",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
 
@@ -47,6 +49,25 @@ class KdaFwdDesc(ctypes.Structure):
         ("num_seqs", ctypes.c_int32), ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int64)),
         ("qkv_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("beta_dtype", ctypes.c_int32),
         ("scale", ctypes.c_float), ("lower_bound", ctypes.c_float), ("flags", ctypes.c_uint32),
+    ]
+
+
+CONV_SILU = 1 << 0
+
+
+class KdaConvDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("W", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32), ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int64)),
+        ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("dy_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32), ("x_stride", ctypes.c_int64),
+    ]
+
+
+class KdaNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("group_size", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
     ]
 
 
@@ -110,6 +131,20 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.kda_chunk_bwd_saved.argtypes = [dp] + [_vp] * 20 + [ctypes.c_size_t, _vp]
     lib.kda_gate_chunk_cumsum.restype = ctypes.c_int
     lib.kda_gate_chunk_cumsum.argtypes = [dp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    cp, np_ = ctypes.POINTER(KdaConvDesc), ctypes.POINTER(KdaNormDesc)
+    size_t = ctypes.c_size_t
+    for name, args in (
+        ("kda_short_conv_fwd", [cp] + [_vp] * 8),
+        ("kda_short_conv_bwd_workspace_size", [cp, szp]),
+        ("kda_short_conv_bwd", [cp] + [_vp] * 12 + [size_t, _vp]),
+        ("kda_short_conv_step", [cp] + [_vp] * 5 + [ctypes.c_int32, _vp, _vp]),
+        ("kda_rms_norm_fwd", [np_] + [_vp] * 6),
+        ("kda_rms_norm_fp8", [np_] + [_vp] * 7),
+        ("kda_rms_norm_bwd_workspace_size", [np_, szp]),
+        ("kda_rms_norm_bwd", [np_] + [_vp] * 7 + [size_t, _vp]),
+    ):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ctypes.c_int, args
     if path == LIBRARY:
         _lib = lib
     return lib

@@ -24,6 +24,7 @@ SOURCES = [
     "kda_recur_c64_bf16.hip", "kda_recur_c64_f32.hip", "kda_recur_c32_bf16.hip", "kda_recur_c32_f32.hip",
     "kda_recurrent.hip", "kda_backward.hip", "kda_noalloc.hip",
     "kda_bwd_chunk_bf16.hip", "kda_bwd_chunk_f32.hip",
+    "kda_layer_abi.cpp", "kda_layer_conv.hip", "kda_layer_norm.hip",
 ]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

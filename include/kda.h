@@ -46,7 +46,7 @@
 extern "C" {
 #endif
 
-#define KDA_ABI_VERSION 4
+#define KDA_ABI_VERSION 5
 
 typedef enum kda_status {
     KDA_OK = 0,
@@ -381,6 +381,115 @@ kda_status kda_gate_chunk_cumsum(const kda_fwd_desc *d, const void *g, const flo
                                  const float *dt_bias, const int64_t *cu_seqlens,
                                  float *g_act, float *g_cum_log2,
                                  void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The operators around the recurrence in a layer.  The conventions above hold, with two
+ * additions: an input that the text below gives a token stride for may be a view whose
+ * tokens lie that many elements apart (the heads and channels of a token stay contiguous;
+ * token b * T + t of the batch begins at (b * T + t) * stride), and outputs must not
+ * overlap inputs unless the text says so.
+ */
+
+/*
+ * The short causal convolution in front of q, k and v (or of a state space scan's x, B and
+ * C): every channel's last W inputs, an optional bias, optional SiLU.
+ *     pre_t = bias + sum_w weight[w] x_{t-W+1+w};   y_t = pre_t, or pre_t * sigmoid(pre_t)
+ * Inputs before a sequence's first token are the rows of its initial state, the W - 1 inputs
+ * that came before (oldest first), or 0.  Sums are fp32.
+ *   B, T, D      batch rows, tokens, channels; W the width, 2, 3 or 4
+ *   num_seqs, cu_seqlens_host   as in kda_fwd_desc
+ *   x_dtype      of x, y, the states and their gradients; w_dtype of weight and bias;
+ *   dy_dtype     of dy: x_dtype, or fp32 (the recurrence's gradients are fp32)
+ *   x_stride     elements between two tokens of x, at least D (y, dy, dx are contiguous)
+ *   flags        KDA_CONV_SILU
+ */
+enum { KDA_CONV_SILU = 1u << 0 };
+typedef struct kda_conv_desc {
+    int32_t B, T, D, W;
+    int32_t num_seqs;
+    const int64_t *cu_seqlens_host;
+    int32_t x_dtype, w_dtype, dy_dtype; /* kda_dtype codes */
+    uint32_t flags;
+    int64_t x_stride;
+} kda_conv_desc;
+
+/*
+ *   x [B, T, D];  weight [D, W];  bias [D] or NULL;  initial_state [num_seqs, W - 1, D] or
+ *   NULL (zeros);  cu_seqlens as kda_chunk_fwd
+ *   y [B, T, D], fully overwritten;  final_state [num_seqs, W - 1, D] or NULL: each
+ *   sequence's last W - 1 inputs (with rows of the initial state where it is shorter); it
+ *   must not be the initial state's memory
+ * Errors: KDA_ERR_SHAPE (sizes; W outside 2..4 is KDA_ERR_UNSUPPORTED), _VARLEN, _DTYPE,
+ * _NULL_POINTER.  Bit for bit the same for a sequence alone and in a pack.
+ */
+kda_status kda_short_conv_fwd(const kda_conv_desc *d, const void *x, const void *weight, const void *bias,
+                              const void *initial_state, const int64_t *cu_seqlens, void *y,
+                              void *final_state, hipStream_t stream);
+
+/*
+ * Gradients of L = <dy, y> + <dht, final_state>; the forward's sums are rebuilt from x.
+ *   dy [B, T, D] dy_dtype;  dht [num_seqs, W - 1, D] x_dtype or NULL (zero)
+ *   dx [B, T, D] x_dtype;  dweight [D, W], dbias [D] (or NULL) fp32;  dh0 [num_seqs, W - 1, D]
+ *   x_dtype or NULL; all fully overwritten
+ * Workspace: kda_short_conv_bwd_workspace_size bytes, 256-byte aligned, contents on entry do
+ * not matter.  No atomics: results do not depend on scheduling.
+ */
+kda_status kda_short_conv_bwd_workspace_size(const kda_conv_desc *d, size_t *bytes);
+kda_status kda_short_conv_bwd(const kda_conv_desc *d, const void *x, const void *weight, const void *bias,
+                              const void *initial_state, const int64_t *cu_seqlens, const void *dy,
+                              const void *dht, void *dx, float *dweight, float *dbias, void *dh0,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token for each of B rows (T must be 1, num_seqs B, no cu_seqlens): y [B, D] from x
+ * [B, D] (rows x_stride apart) and the rows' states, which move on in place.
+ *   state  [num_slots, W - 1, D] x_dtype
+ *   slots  [B] int32 device: the state of each row, or NULL (row b has slot b; then num_slots
+ *          must be at least B).  A slot below 0 or past the pool marks a padding row: its y is
+ *          0 and no state is touched.  Two rows must not share a slot: what such rows and
+ *          that slot then hold is undefined (no access leaves the pool).
+ */
+kda_status kda_short_conv_step(const kda_conv_desc *d, const void *x, const void *weight, const void *bias,
+                               void *state, const int32_t *slots, int32_t num_slots, void *y,
+                               hipStream_t stream);
+
+/*
+ * RMS norm of rows of D values with the residual's addition in front.
+ *     h = x + residual, rounded to x_dtype;   y = h * (mean(h^2) + eps)^(-1/2) * weight
+ *   rows, D      D at most 32768
+ *   group_size   of kda_rms_norm_fp8: values under one scale, 0 for the whole row, else a
+ *                power of two of 8..512 that divides D
+ *   x_dtype      of x, residual, h, y and the gradients dy, dh, dx; w_dtype of weight
+ */
+typedef struct kda_norm_desc {
+    int64_t rows;
+    int32_t D, group_size;
+    int32_t x_dtype, w_dtype; /* kda_dtype codes */
+    float eps;
+} kda_norm_desc;
+
+/*   x, residual (or NULL) [rows, D];  weight [D];  y [rows, D];  h [rows, D] or NULL */
+kda_status kda_rms_norm_fwd(const kda_norm_desc *d, const void *x, const void *residual, const void *weight,
+                            void *y, void *h, hipStream_t stream);
+
+/*
+ * The same norm with y in 8 bits (e4m3): over each group scale = max|y| / 448 and
+ * q = round(y / scale) (to nearest even; y itself is not rounded before).  A group whose
+ * values are all 0 has scale 1e-30 / 448; one with a NaN has a NaN scale.
+ *   q [rows, D] bytes;  scales [rows, D / group_size] (or [rows, 1]) fp32;  h as above
+ */
+kda_status kda_rms_norm_fp8(const kda_norm_desc *d, const void *x, const void *residual, const void *weight,
+                            void *q, float *scales, void *h, hipStream_t stream);
+
+/*
+ * Gradients of <dy, y> + <dh, h> by h (x and the residual each get it) and by the weight:
+ *   h, dy [rows, D];  dh [rows, D] or NULL (zero);  dx [rows, D] x_dtype;  dweight [D] fp32
+ * Workspace and determinism as kda_short_conv_bwd.
+ */
+kda_status kda_rms_norm_bwd_workspace_size(const kda_norm_desc *d, size_t *bytes);
+kda_status kda_rms_norm_bwd(const kda_norm_desc *d, const void *h, const void *weight, const void *dy,
+                            const void *dh, void *dx, float *dweight, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
