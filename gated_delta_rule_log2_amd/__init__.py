@@ -27,7 +27,7 @@ from . import _abi
 
 __all__ = ["chunk_kda", "chunk_kda_bwd", "fused_recurrent_kda", "gate_chunk_cumsum", "KDAContractError", "KDARuntimeError",
            "workspace_bytes", "library", "short_conv", "short_conv_bwd", "short_conv_step", "rms_norm", "rms_norm_fp8",
-           "rms_norm_bwd"]
+           "rms_norm_bwd", "chunk_ssm", "chunk_ssm_bwd", "ssm_step"]
 
 
 class KDAContractError(ValueError):
@@ -450,5 +450,5 @@ def gate_chunk_cumsum(g: torch.Tensor, *, chunk_size: int = 64, use_gate_in_kern
     return g_act, g_cum
 
 
-from .layers import (rms_norm, rms_norm_bwd, rms_norm_fp8, short_conv, short_conv_bwd,  # noqa: E402
-                     short_conv_step)
+from .layers import (chunk_ssm, chunk_ssm_bwd, rms_norm, rms_norm_bwd, rms_norm_fp8, short_conv,  # noqa: E402
+                     short_conv_bwd, short_conv_step, ssm_step)

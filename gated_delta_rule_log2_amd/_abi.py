@@ -38,6 +38,7 @@ EXPORTS = (
     "kda_chunk_bwd_saved",
     "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_size", "kda_short_conv_bwd", "kda_short_conv_step",
     "kda_rms_norm_fwd", "kda_rms_norm_fp8", "kda_rms_norm_bwd_workspace_size", "kda_rms_norm_bwd",
+    "kda_ssm_fwd_workspace_size", "kda_ssm_fwd", "kda_ssm_bwd_workspace_size", "kda_ssm_bwd", "kda_ssm_step",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
 
@@ -68,6 +69,19 @@ class KdaNormDesc(ctypes.Structure):
     _fields_ = [
         ("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("group_size", ctypes.c_int32),
         ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+    ]
+
+
+SSM_SOFTPLUS = 1 << 0
+
+
+class KdaSsmDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("G", ctypes.c_int32),
+        ("N", ctypes.c_int32), ("P", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+        ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int64)), ("x_dtype", ctypes.c_int32),
+        ("dt_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("x_stride", ctypes.c_int64),
+        ("dt_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
     ]
 
 
@@ -131,7 +145,7 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.kda_chunk_bwd_saved.argtypes = [dp] + [_vp] * 20 + [ctypes.c_size_t, _vp]
     lib.kda_gate_chunk_cumsum.restype = ctypes.c_int
     lib.kda_gate_chunk_cumsum.argtypes = [dp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
-    cp, np_ = ctypes.POINTER(KdaConvDesc), ctypes.POINTER(KdaNormDesc)
+    cp, np_, sp = (ctypes.POINTER(t) for t in (KdaConvDesc, KdaNormDesc, KdaSsmDesc))
     size_t = ctypes.c_size_t
     for name, args in (
         ("kda_short_conv_fwd", [cp] + [_vp] * 8),
@@ -142,6 +156,11 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
         ("kda_rms_norm_fp8", [np_] + [_vp] * 7),
         ("kda_rms_norm_bwd_workspace_size", [np_, szp]),
         ("kda_rms_norm_bwd", [np_] + [_vp] * 7 + [size_t, _vp]),
+        ("kda_ssm_fwd_workspace_size", [sp, szp]),
+        ("kda_ssm_fwd", [sp] + [_vp] * 12 + [size_t, _vp]),
+        ("kda_ssm_bwd_workspace_size", [sp, szp]),
+        ("kda_ssm_bwd", [sp] + [_vp] * 20 + [size_t, _vp]),
+        ("kda_ssm_step", [sp] + [_vp] * 9 + [ctypes.c_int32, _vp, _vp]),
     ):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, args

@@ -25,6 +25,7 @@ SOURCES = [
     "kda_recurrent.hip", "kda_backward.hip", "kda_noalloc.hip",
     "kda_bwd_chunk_bf16.hip", "kda_bwd_chunk_f32.hip",
     "kda_layer_abi.cpp", "kda_layer_conv.hip", "kda_layer_norm.hip",
+    "kda_layer_ssm_fwd.hip", "kda_layer_ssm_bwd.hip",
 ]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -45,4 +45,36 @@ int norm_bwd_blocks(const NormParams &p);
 hipError_t launch_norm_fwd(const NormParams &p, bool fp8, hipStream_t s);
 hipError_t launch_norm_bwd(const NormParams &p, hipStream_t s);
 
+// The state space scan.  L tokens make a chunk (chunks restart at every sequence), `seg`
+// chunks of one sequence a segment, whose states one workgroup carries.
+struct SsmParams {
+    int32_t B, T, H, G, N, P, NS;  // NS = sequences
+    int32_t L, total_chunks, seg, total_segs, max_segs;  // max_segs: of one sequence
+    int32_t x_bf16, dt_bf16, softplus;
+    int32_t num_slots;
+    int32_t split;                 // backward: parts of a group's heads, each with its own sums for dB, dC
+    int64_t tokens;                // B * T
+    int64_t x_stride, dt_stride, b_stride, c_stride;
+    const void *x, *dt, *Bm, *C, *dy;
+    const float *A_log, *D, *dt_bias, *h0, *dht;
+    const int64_t *cu_seqlens;
+    const int32_t *slots;
+    void *y, *dx, *ddt, *dB, *dC;
+    float *ht, *dh0, *dA_log, *dD, *ddt_bias, *state;
+    // workspace
+    int4 *chunk;                   // [total_chunks] first token, length, sequence
+    float *d, *ch, *cl, *fs, *fe;  // [total_chunks][H][L]: see ssm_prep_kernel
+    float *dec;                    // [total_chunks][H] the chunk's whole decay
+    void *S[2], *R[2];             // [total_chunks][H] states in fragment order, high and low parts
+    float *seg_end;                // [2][total_segs][H] N * P each: states of segments from zero
+    float *seg_dec;                // [2][total_segs][H]
+    float *sums;                   // backward: [total_chunks][H][4] terms of dA_log, ddt_bias, dD
+    float *dBp, *dCp;              // backward: [split][tokens][G][N] where split > 1
+};
+
+size_t ssm_workspace(SsmParams &p, void *ws, bool backward);  // sizes (and, with ws, binds) the workspace
+hipError_t launch_ssm_fwd(const SsmParams &p, hipStream_t s);
+hipError_t launch_ssm_bwd(const SsmParams &p, hipStream_t s);
+hipError_t launch_ssm_step(const SsmParams &p, hipStream_t s);
+
 }  // namespace kda

@@ -1,5 +1,5 @@
 // kda_layer_abi.cpp -- the C ABI of the operators around the recurrence (short convolution,
-// RMS norm) declared in include/kda.h: argument checks, workspace layout, launches.  The
+// RMS norm, state space scan) declared in include/kda.h: argument checks, workspace layout, launches.  The
 // checks come before any HIP call, descriptor first, then pointers, then the workspace.
 #include <hip/hip_runtime.h>
 
@@ -68,10 +68,115 @@ kda_status check_norm(const kda_norm_desc *d, bool fp8, NormParams &p) {
     return KDA_OK;
 }
 
+constexpr int64_t kCarryGroups = 512;  // workgroups wanted of a pass over chunks: two for each CU
+constexpr int64_t kBwdGroups = 512;    // and of the backward's chunk kernel
+
+kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {
+    if (!d) return KDA_ERR_NULL_POINTER;
+    if (d->B < 1 || d->T < 0 || d->H < 1 || d->G < 1 || d->N < 1 || d->P < 1 || d->num_seqs < 0) return KDA_ERR_SHAPE;
+    if ((int64_t)d->B * d->T > (int64_t)INT32_MAX / 2 || d->H > (1 << 20)) return KDA_ERR_SHAPE;
+    if (d->N % 32 || d->N > 128 || d->P % 32 || d->P > 128 || (d->flags & ~(uint32_t)KDA_SSM_SOFTPLUS)) return KDA_ERR_UNSUPPORTED;
+    if (d->H % d->G) return KDA_ERR_GVA;
+    if (d->x_stride < (int64_t)d->H * d->P || d->dt_stride < d->H || d->b_stride < (int64_t)d->G * d->N ||
+        d->c_stride < (int64_t)d->G * d->N)
+        return KDA_ERR_SHAPE;
+    const kda_status st = check_seqs(d->B, d->T, d->num_seqs, d->cu_seqlens_host);
+    if (st != KDA_OK) return st;
+    if (!dtype_ok(d->x_dtype) || !dtype_ok(d->dt_dtype)) return KDA_ERR_DTYPE;
+    std::memset(&p, 0, sizeof(p));
+    p.B = d->B; p.T = d->T; p.H = d->H; p.G = d->G; p.N = d->N; p.P = d->P; p.NS = d->num_seqs;
+    p.tokens = (int64_t)d->B * d->T;
+    p.x_bf16 = d->x_dtype == KDA_DTYPE_BF16;
+    p.dt_bf16 = d->dt_dtype == KDA_DTYPE_BF16;
+    p.softplus = (d->flags & KDA_SSM_SOFTPLUS) ? 1 : 0;
+    p.x_stride = d->x_stride; p.dt_stride = d->dt_stride; p.b_stride = d->b_stride; p.c_stride = d->c_stride;
+    p.L = p.x_bf16 ? 64 : 32;
+    return KDA_OK;
+}
+
+// The chunks, and how many of them make a segment: enough segments that the passes over chunks
+// fill the GPU, and at least four chunks in each (joining a segment costs about one).
+kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p, bool backward) {
+    auto each = [&](auto f) {
+        if (d->cu_seqlens_host)
+            for (int32_t n = 0; n < p.NS; ++n) f((d->cu_seqlens_host[n + 1] - d->cu_seqlens_host[n] + p.L - 1) / p.L, 1);
+        else f((int64_t)(p.T + p.L - 1) / p.L, p.NS);
+    };
+    int64_t chunks = 0, segs = 0, most = 1;
+    each([&](int64_t c, int64_t times) { chunks += c * times; });
+    const int64_t tiles = ((backward ? p.N : p.P) + 63) / 64;
+    if (chunks * p.H > INT32_MAX) return KDA_ERR_SHAPE;
+    const int64_t seg = (chunks * p.H * tiles + kCarryGroups - 1) / kCarryGroups;
+    p.seg = (int32_t)(seg < 4 ? 4 : seg);
+    each([&](int64_t c, int64_t times) {
+        const int64_t s = c > p.seg ? (c + p.seg - 1) / p.seg : 1;
+        segs += s * times;
+        if (s > most) most = s;
+    });
+    if (segs * p.H * tiles * 2 > INT32_MAX - 8) return KDA_ERR_SHAPE;
+    p.total_chunks = (int32_t)chunks; p.total_segs = (int32_t)segs; p.max_segs = (int32_t)most;
+    const int32_t hg = p.H / p.G;
+    const int64_t groups = chunks * p.G > 0 ? chunks * p.G : 1;
+    int64_t split = groups < kBwdGroups ? (kBwdGroups + groups - 1) / groups : 1;
+    if (split > hg) split = hg;
+    const int32_t per = (int32_t)((hg + split - 1) / split);
+    p.split = (hg + per - 1) / per;
+    return KDA_OK;
+}
+
 }  // namespace
+
+size_t ssm_workspace(SsmParams &p, void *ws, bool backward) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char *at = ws ? static_cast<unsigned char *>(ws) + off : nullptr;
+        off += (bytes + 255) / 256 * 256;
+        return static_cast<void *>(at);
+    };
+    const size_t ch = (size_t)p.total_chunks * p.H, tok = ch * p.L * sizeof(float), eb = p.x_bf16 ? 2 : 4;
+    const size_t state = (size_t)p.N * p.P, dirs = backward ? 2 : 1;
+    p.chunk = static_cast<int4 *>(take((size_t)p.total_chunks * sizeof(int4)));
+    p.d = static_cast<float *>(take(tok));
+    p.ch = static_cast<float *>(take(tok));
+    p.cl = static_cast<float *>(take(tok));
+    p.fs = static_cast<float *>(take(tok));
+    p.fe = static_cast<float *>(take(tok));
+    p.dec = static_cast<float *>(take(ch * sizeof(float)));
+    const int parts = backward && p.x_bf16 ? 2 : 1;
+    for (int i = 0; i < parts; ++i) p.S[i] = take(ch * state * eb);
+    for (int i = 0; backward && i < parts; ++i) p.R[i] = take(ch * state * eb);
+    if (p.max_segs > 1) {
+        p.seg_end = static_cast<float *>(take(dirs * p.total_segs * p.H * state * sizeof(float)));
+        p.seg_dec = static_cast<float *>(take(dirs * p.total_segs * p.H * sizeof(float)));
+    }
+    if (backward) {
+        p.sums = static_cast<float *>(take(ch * 4 * sizeof(float)));
+        if (p.split > 1) {
+            const size_t part = (size_t)p.split * p.tokens * p.G * p.N * sizeof(float);
+            p.dBp = static_cast<float *>(take(part));
+            p.dCp = static_cast<float *>(take(part));
+        }
+    }
+    return off ? off : 256;
+}
+
 }  // namespace kda
 
 using namespace kda;
+
+static kda_status ssm_prepare(const kda_ssm_desc *d, SsmParams &p, bool backward) {
+    const kda_status st = check_ssm(d, p);
+    return st == KDA_OK ? plan_ssm(d, p, backward) : st;
+}
+
+static kda_status ssm_size(const kda_ssm_desc *d, size_t *bytes, bool backward) {
+    SsmParams p;
+    const kda_status st = ssm_prepare(d, p, backward);
+    if (st != KDA_OK) return st;
+    if (!bytes) return KDA_ERR_NULL_POINTER;
+    *bytes = ssm_workspace(p, nullptr, backward);
+    return KDA_OK;
+}
 
 extern "C" {
 
@@ -172,6 +277,60 @@ kda_status kda_rms_norm_bwd(const kda_norm_desc *d, const void *h, const void *w
     p.x = h; p.weight = weight; p.dy = dy; p.dh = dh; p.dx = dx; p.dweight = dweight;
     p.partial = static_cast<float *>(workspace);
     return to_status(launch_norm_bwd(p, stream));
+}
+
+kda_status kda_ssm_fwd_workspace_size(const kda_ssm_desc *d, size_t *bytes) { return ssm_size(d, bytes, false); }
+kda_status kda_ssm_bwd_workspace_size(const kda_ssm_desc *d, size_t *bytes) { return ssm_size(d, bytes, true); }
+
+kda_status kda_ssm_fwd(const kda_ssm_desc *d, const void *x, const void *dt, const float *A_log, const void *Bm,
+                       const void *C, const float *D, const float *dt_bias, const float *initial_state,
+                       const int64_t *cu_seqlens, void *y, float *final_state, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+    SsmParams p;
+    const kda_status st = ssm_prepare(d, p, false);
+    if (st != KDA_OK) return st;
+    if (p.tokens > 0 && (!x || !dt || !Bm || !C || !y)) return KDA_ERR_NULL_POINTER;
+    if (!A_log) return KDA_ERR_MISSING_A_LOG;
+    if ((cu_seqlens == nullptr) != (d->cu_seqlens_host == nullptr)) return KDA_ERR_VARLEN;
+    if (final_state && final_state == initial_state) return KDA_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < ssm_workspace(p, workspace, false)) return KDA_ERR_WORKSPACE;
+    p.x = x; p.dt = dt; p.A_log = A_log; p.Bm = Bm; p.C = C; p.D = D; p.dt_bias = dt_bias; p.h0 = initial_state;
+    p.cu_seqlens = cu_seqlens; p.y = y; p.ht = final_state;
+    return to_status(launch_ssm_fwd(p, stream));
+}
+
+kda_status kda_ssm_bwd(const kda_ssm_desc *d, const void *x, const void *dt, const float *A_log, const void *Bm,
+                       const void *C, const float *D, const float *dt_bias, const float *initial_state,
+                       const int64_t *cu_seqlens, const void *dy, const float *dht, void *dx, void *ddt,
+                       float *dA_log, void *dB, void *dC, float *dD, float *ddt_bias, float *dh0, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+    SsmParams p;
+    const kda_status st = ssm_prepare(d, p, true);
+    if (st != KDA_OK) return st;
+    if (p.tokens > 0 && (!x || !dt || !Bm || !C || !dy || !dx || !ddt || !dB || !dC)) return KDA_ERR_NULL_POINTER;
+    if (!dA_log) return KDA_ERR_NULL_POINTER;
+    if (!A_log) return KDA_ERR_MISSING_A_LOG;
+    if ((cu_seqlens == nullptr) != (d->cu_seqlens_host == nullptr)) return KDA_ERR_VARLEN;
+    if (!workspace || workspace_bytes < ssm_workspace(p, workspace, true)) return KDA_ERR_WORKSPACE;
+    p.x = x; p.dt = dt; p.A_log = A_log; p.Bm = Bm; p.C = C; p.D = D; p.dt_bias = dt_bias; p.h0 = initial_state;
+    p.cu_seqlens = cu_seqlens; p.dy = dy; p.dht = dht;
+    p.dx = dx; p.ddt = ddt; p.dA_log = dA_log; p.dB = dB; p.dC = dC; p.dD = dD; p.ddt_bias = ddt_bias; p.dh0 = dh0;
+    return to_status(launch_ssm_bwd(p, stream));
+}
+
+kda_status kda_ssm_step(const kda_ssm_desc *d, const void *x, const void *dt, const float *A_log, const void *Bm,
+                        const void *C, const float *D, const float *dt_bias, float *state, const int32_t *slots,
+                        int32_t num_slots, void *y, hipStream_t stream) {
+    SsmParams p;
+    const kda_status st = check_ssm(d, p);
+    if (st != KDA_OK) return st;
+    if (p.T != 1 || num_slots < 0 || (!slots && num_slots < p.B)) return KDA_ERR_SHAPE;
+    if (d->cu_seqlens_host) return KDA_ERR_VARLEN;
+    if (!x || !dt || !Bm || !C || !y || (num_slots > 0 && !state)) return KDA_ERR_NULL_POINTER;
+    if (!A_log) return KDA_ERR_MISSING_A_LOG;
+    p.x = x; p.dt = dt; p.A_log = A_log; p.Bm = Bm; p.C = C; p.D = D; p.dt_bias = dt_bias;
+    p.state = state; p.slots = slots; p.num_slots = num_slots; p.y = y;
+    return to_status(launch_ssm_step(p, stream));
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
-"""The operators around the recurrence in a layer: the short causal convolution and the RMS
-norm with the residual's addition, each for prompts, for single tokens and for gradients.
+"""The operators around the recurrence in a layer: the short causal convolution, the RMS norm
+with the residual's addition, and the selective state space scan that takes the recurrence's
+place in some layers; each for prompts, for single tokens and for gradients.
 
 As in the rest of the package the work is the HIP library's (C ABI in include/kda.h); the
 functions here check and marshal torch tensors, run on the current HIP stream of the
@@ -8,6 +9,8 @@ except that a packed call without ``cu_seqlens_host`` reads its offsets (as chun
 
     y, state = short_conv(x, weight, bias, activation="silu", output_final_state=True)
     y = short_conv_step(x_t, state, weight, bias, activation="silu")
+    y, state = chunk_ssm(x, dt, A_log, B, C, output_final_state=True)
+    y = ssm_step(x_t, dt_t, A_log, B_t, C_t, state)
     y, h = rms_norm(x, weight, residual)
     q, scales, h = rms_norm_fp8(x, weight, residual, group_size=128)
 """
@@ -274,3 +277,118 @@ def rms_norm_bwd(h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, dh: Op
     _call(lib.kda_rms_norm_bwd, dev, _byref(d), _ptr(h), _ptr(weight), _ptr(dy), _ptr(dh), _ptr(dx), _ptr(dweight),
           _ptr(ws), ws.numel())
     return {"dx": dx, "dweight": dweight}
+
+
+# ------------------------------------------------------------------------------- state space scan
+def _ssm_desc(x, dt, A_log, B, C, D, dt_bias, softplus, offsets, what):
+    dev = x.device
+    nb, T, H, P = x.shape
+    d = _abi.KdaSsmDesc()
+    d.B, d.T, d.H, d.P = nb, T, H, P
+    d.G, d.N = B.shape[2:]
+    d.num_seqs, d.cu_seqlens_host = offsets.N, offsets.host_ptr
+    d.x_dtype, d.dt_dtype = _dtype_code(x, "x"), _dtype_code(dt, "dt")
+    d.flags = _abi.SSM_SOFTPLUS if softplus else 0
+    d.x_stride = _token_stride(x, "x", (nb, T, H, P), dev)
+    d.dt_stride = _token_stride(dt, "dt", (nb, T, H), dev)
+    d.b_stride = _token_stride(B, "B", (nb, T, d.G, d.N), dev, x.dtype)
+    d.c_stride = _token_stride(C, "C", (nb, T, d.G, d.N), dev, x.dtype)
+    if A_log is None:
+        _refuse("KDA_ERR_MISSING_A_LOG", f"{what} needs A_log")
+    for t, name in ((A_log, "A_log"), (D, "D"), (dt_bias, "dt_bias")):
+        _check_tensor(t, name, (H,), dev, torch.float32)
+    return d
+
+
+def _ssm_shapes(x, dt, B, C, dims, what):
+    if x.dim() != dims or B.dim() != dims or C.dim() != dims or dt.dim() != dims - 1 or x.shape[0] < 1:
+        _refuse("KDA_ERR_SHAPE", "x must be [B, T, H, P], dt [B, T, H], and B, C [B, T, G, N] (a step has no T)")
+    if 0 in x.shape[-2:] or 0 in B.shape[-2:]:
+        _refuse("KDA_ERR_SHAPE", "x, B and C must have heads and channels")
+    return _device(x, what)
+
+
+def chunk_ssm(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+              D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+              use_softplus_in_kernel: bool = False, initial_state: Optional[torch.Tensor] = None,
+              output_final_state: bool = False, cu_seqlens: Optional[torch.Tensor] = None, *,
+              cu_seqlens_host: Optional[torch.Tensor] = None):
+    """The selective state space scan: per head, with the step d_t = dt_t + dt_bias (through a
+    softplus with use_softplus_in_kernel) and A = -exp(A_log),
+
+        S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T;    y_t = S_t^T C_t + D x_t
+
+    Returns (y, final_state or None).  x [B, T, H, P], B, C [B, T, G, N] (head h uses group
+    h / (H / G)) in one of float32 and bfloat16, dt [B, T, H] in either; each may be a view
+    whose tokens are evenly spaced.  A_log, D, dt_bias [H] float32; N and P multiples of 32 up
+    to 128.  initial_state / final_state [N_seq, H, N, P] float32 (N_seq = B, or
+    len(cu_seqlens) - 1 with B = 1).  cu_seqlens_host as short_conv.
+    """
+    dev = _ssm_shapes(x, dt, B, C, 4, "chunk_ssm")
+    offsets = _Offsets(cu_seqlens, cu_seqlens_host, x.shape[0], dev)
+    d = _ssm_desc(x, dt, A_log, B, C, D, dt_bias, use_softplus_in_kernel, offsets, "chunk_ssm")
+    states = (offsets.N, d.H, d.N, d.P)
+    _check_tensor(initial_state, "initial_state", states, dev, torch.float32)
+    lib = library()
+    ws = _scratch(_size(lib.kda_ssm_fwd_workspace_size, d), dev)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    ht = torch.empty(states, dtype=torch.float32, device=dev) if output_final_state else None
+    _call(lib.kda_ssm_fwd, dev, _byref(d), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias),
+          _ptr(initial_state), _ptr(offsets.dev), _ptr(y), _ptr(ht), _ptr(ws), ws.numel())
+    return y, ht
+
+
+def chunk_ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                  dy: torch.Tensor, dht: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
+                  dt_bias: Optional[torch.Tensor] = None, use_softplus_in_kernel: bool = False,
+                  initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                  cu_seqlens_host: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of <dy, y> + <dht, final_state> for chunk_ssm's inputs: dx, dB, dC in x's
+    dtype, ddt in dt's, dA_log, and dD, ddt_bias, dh0 where D, dt_bias, an initial_state are
+    given, in float32.  dy has x's shape and dtype (contiguous), dht the final state's.
+    """
+    dev = _ssm_shapes(x, dt, B, C, 4, "chunk_ssm_bwd")
+    offsets = _Offsets(cu_seqlens, cu_seqlens_host, x.shape[0], dev)
+    d = _ssm_desc(x, dt, A_log, B, C, D, dt_bias, use_softplus_in_kernel, offsets, "chunk_ssm_bwd")
+    states = (offsets.N, d.H, d.N, d.P)
+    _check_tensor(dy, "dy", x.shape, dev, x.dtype)
+    _check_tensor(initial_state, "initial_state", states, dev, torch.float32)
+    _check_tensor(dht, "dht", states, dev, torch.float32)
+    lib = library()
+    ws = _scratch(_size(lib.kda_ssm_bwd_workspace_size, d), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "ddt": torch.empty(dt.shape, dtype=dt.dtype, device=dev),
+           "dA_log": torch.empty((d.H,), **f32), "dB": torch.empty(B.shape, dtype=x.dtype, device=dev),
+           "dC": torch.empty(C.shape, dtype=x.dtype, device=dev)}
+    if D is not None:
+        out["dD"] = torch.empty((d.H,), **f32)
+    if dt_bias is not None:
+        out["ddt_bias"] = torch.empty((d.H,), **f32)
+    if initial_state is not None:
+        out["dh0"] = torch.empty(states, **f32)
+    _call(lib.kda_ssm_bwd, dev, _byref(d), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias),
+          _ptr(initial_state), _ptr(offsets.dev), _ptr(dy), _ptr(dht), _ptr(out["dx"]), _ptr(out["ddt"]),
+          _ptr(out["dA_log"]), _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out.get("dD")), _ptr(out.get("ddt_bias")),
+          _ptr(out.get("dh0")), _ptr(ws), ws.numel())
+    return out
+
+
+def ssm_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+             state: torch.Tensor, D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+             use_softplus_in_kernel: bool = False, slots: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of each row: y [rows, H, P] from x [rows, H, P], dt [rows, H], B, C [rows, G, N]
+    and the rows' states, updated in place.  state [pool, H, N, P] float32; slots as
+    short_conv_step.
+    """
+    if x.dim() == 3 and x.shape[0] == 0:
+        return torch.empty_like(x)
+    dev = _ssm_shapes(x, dt, B, C, 3, "ssm_step")
+    rows = x.shape[0]
+    d = _ssm_desc(x.unsqueeze(1), dt.unsqueeze(1), A_log, B.unsqueeze(1), C.unsqueeze(1), D, dt_bias,
+                  use_softplus_in_kernel, _Offsets(None, None, rows, dev), "ssm_step")
+    _check_tensor(state, "state", (state.shape[0], d.H, d.N, d.P), dev, torch.float32)
+    _slots(slots, rows, state.shape[0], dev)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    _call(library().kda_ssm_step, dev, _byref(d), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
+          _ptr(dt_bias), _ptr(state), _ptr(slots), state.shape[0], _ptr(y))
+    return y

@@ -491,6 +491,72 @@ kda_status kda_rms_norm_bwd(const kda_norm_desc *d, const void *h, const void *w
                             const void *dh, void *dx, float *dweight, void *workspace,
                             size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * The selective state space scan: the recurrence with one input-dependent decay per head and
+ * no delta rule.  For each sequence and head h (group g = h / (H / G) of B and C), with the
+ * step d_t = softplus(dt_t + dt_bias[h]) (or dt_t + dt_bias[h]) and A = -exp(A_log[h]):
+ *     S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T;    y_t = S_t^T C_t + D[h] x_t
+ * computed over chunks of 64 tokens (32 with fp32 inputs) as matrix products, and chunks of
+ * long sequences in segments side by side whose states are joined.  States and sums are fp32.
+ *   B, T         batch rows and tokens; H heads, G groups (H % G == 0)
+ *   N, P         state rows and head size, multiples of 32 up to 128
+ *   num_seqs, cu_seqlens_host   as in kda_fwd_desc
+ *   x_dtype      of x, B, C, y and dy, dx, dB, dC;  dt_dtype of dt and ddt
+ *   x_stride, dt_stride, b_stride, c_stride   elements between two tokens (at least H * P, H,
+ *                G * N, G * N); y and every gradient are contiguous
+ *   flags        KDA_SSM_SOFTPLUS
+ * A token's decay below 2^-200 is taken as that (0 in fp32).  A NaN or infinity in a token
+ * reaches the later tokens of its sequence, and may reach earlier ones of its chunk; it never
+ * reaches another sequence.
+ */
+enum { KDA_SSM_SOFTPLUS = 1u << 0 };
+typedef struct kda_ssm_desc {
+    int32_t B, T, H, G, N, P;
+    int32_t num_seqs;
+    const int64_t *cu_seqlens_host;
+    int32_t x_dtype, dt_dtype; /* kda_dtype codes */
+    uint32_t flags;
+    int64_t x_stride, dt_stride, b_stride, c_stride;
+} kda_ssm_desc;
+
+/*
+ *   x [B, T, H, P];  dt [B, T, H];  A_log [H] fp32;  Bm, C [B, T, G, N];  D, dt_bias [H] fp32
+ *   or NULL (0);  initial_state [num_seqs, H, N, P] fp32 or NULL (zeros)
+ *   y [B, T, H, P], fully overwritten;  final_state [num_seqs, H, N, P] fp32 or NULL; it must
+ *   not be the initial state's memory
+ * Workspace: kda_ssm_fwd_workspace_size bytes, 256-byte aligned; contents on entry do not
+ * matter.  Errors: KDA_ERR_SHAPE, _GVA (H not a multiple of G), _UNSUPPORTED (N or P), _VARLEN,
+ * _DTYPE, _MISSING_A_LOG, _NULL_POINTER, _WORKSPACE.
+ */
+kda_status kda_ssm_fwd_workspace_size(const kda_ssm_desc *d, size_t *bytes);
+kda_status kda_ssm_fwd(const kda_ssm_desc *d, const void *x, const void *dt, const float *A_log, const void *Bm,
+                       const void *C, const float *D, const float *dt_bias, const float *initial_state,
+                       const int64_t *cu_seqlens, void *y, float *final_state, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of L = <dy, y> + <dht, final_state> for every input; the states are rebuilt.
+ *   dy [B, T, H, P] x_dtype;  dht [num_seqs, H, N, P] fp32 or NULL (zero)
+ *   dx [B, T, H, P], dB, dC [B, T, G, N] x_dtype;  ddt [B, T, H] dt_dtype;  dA_log [H] fp32;
+ *   dD, ddt_bias [H] fp32 or NULL;  dh0 [num_seqs, H, N, P] fp32 or NULL; fully overwritten
+ * Workspace kda_ssm_bwd_workspace_size.  No atomics: results do not depend on scheduling.
+ */
+kda_status kda_ssm_bwd_workspace_size(const kda_ssm_desc *d, size_t *bytes);
+kda_status kda_ssm_bwd(const kda_ssm_desc *d, const void *x, const void *dt, const float *A_log, const void *Bm,
+                       const void *C, const float *D, const float *dt_bias, const float *initial_state,
+                       const int64_t *cu_seqlens, const void *dy, const float *dht, void *dx, void *ddt,
+                       float *dA_log, void *dB, void *dC, float *dD, float *ddt_bias, float *dh0,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token for each of B rows (T must be 1, num_seqs B, no cu_seqlens): y [B, H, P] from x
+ * [B, H, P], dt [B, H], Bm, C [B, G, N] (strides as above) and the rows' states, updated in
+ * place.  state [num_slots, H, N, P] fp32, 16-byte aligned; slots as kda_short_conv_step.
+ */
+kda_status kda_ssm_step(const kda_ssm_desc *d, const void *x, const void *dt, const float *A_log, const void *Bm,
+                        const void *C, const float *D, const float *dt_bias, float *state, const int32_t *slots,
+                        int32_t num_slots, void *y, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

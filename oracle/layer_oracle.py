@@ -92,3 +92,65 @@ def e4m3_values():
     pos = [m * 2.0 ** -9 for m in range(8)] + [2.0 ** (e - 7) * (1 + m / 8) for e in range(1, 16) for m in range(8)]
     pos = pos[:-1]  # the last code is NaN
     return torch.tensor([-v for v in pos[:0:-1]] + pos, dtype=F64)
+
+
+def ssm_steps(dt, dt_bias=None, softplus=False):
+    raw = f64(dt) + (0 if dt_bias is None else f64(dt_bias))
+    return torch.nn.functional.softplus(raw, threshold=1e9) if softplus else raw, raw
+
+
+def _ssm_rows(x, d, A, B, C, h0, cu):
+    """Each sequence's tokens, with B and C for every head and its first state."""
+    H, G = x.shape[2], B.shape[2]
+    Bh, Ch = B.repeat_interleave(H // G, 2), C.repeat_interleave(H // G, 2)
+    for n, (r, a, b) in enumerate(spans(x.shape[0], x.shape[1], cu)):
+        S = torch.zeros(H, B.shape[3], x.shape[3], dtype=F64) if h0 is None else h0[n].clone()
+        yield n, r, a, b, S, Bh, Ch
+
+
+def ssm(x, dt, A_log, B, C, D=None, dt_bias=None, softplus=False, h0=None, cu=None, D_sign=1.0):
+    """y and the final states of S_t = e^{d A} S + d B x^T, y = S^T C + D x, token by token."""
+    d, _ = ssm_steps(dt, dt_bias, softplus)
+    x, B, C, h0, A = f64(x), f64(B), f64(C), f64(h0), -torch.exp(f64(A_log))
+    y = torch.zeros_like(x)
+    n_seq = len(spans(x.shape[0], x.shape[1], cu))
+    last = torch.zeros(n_seq, x.shape[2], B.shape[3], x.shape[3], dtype=F64)
+    for n, r, a, b, S, Bh, Ch in _ssm_rows(x, d, A, B, C, h0, cu):
+        for t in range(a, b):
+            S = torch.exp(d[r, t] * A)[:, None, None] * S + d[r, t, :, None, None] * Bh[r, t][:, :, None] * x[r, t][:, None, :]
+            y[r, t] = (S * Ch[r, t][:, :, None]).sum(1)
+        last[n] = S
+    return (y if D is None else y + f64(D)[:, None] * x), last
+
+
+def ssm_bwd(x, dt, A_log, B, C, dy, dht=None, D=None, dt_bias=None, softplus=False, h0=None, cu=None):
+    """The gradients of <dy, y> + <dht, final states> by the adjoint recurrence.  `dl` is the
+    gradient by each decay's logarithm, `direct` the one by d through d B x^T."""
+    d, raw = ssm_steps(dt, dt_bias, softplus)
+    x, B, C, dy, h0, dht, A = f64(x), f64(B), f64(C), f64(dy), f64(h0), f64(dht), -torch.exp(f64(A_log))
+    H, G = x.shape[2], B.shape[2]
+    dx, dl, direct = torch.zeros_like(x), torch.zeros_like(d), torch.zeros_like(d)
+    dBh = torch.zeros(*B.shape[:2], H, B.shape[3], dtype=F64)
+    dCh = torch.zeros_like(dBh)
+    dh0 = torch.zeros(len(spans(x.shape[0], x.shape[1], cu)), H, B.shape[3], x.shape[3], dtype=F64)
+    for n, r, a, b, S, Bh, Ch in _ssm_rows(x, d, A, B, C, h0, cu):
+        states = [S]
+        for t in range(a, b):
+            states.append(torch.exp(d[r, t] * A)[:, None, None] * states[-1]
+                          + d[r, t, :, None, None] * Bh[r, t][:, :, None] * x[r, t][:, None, :])
+        R = torch.zeros_like(S) if dht is None else dht[n].clone()
+        for t in range(b - 1, a - 1, -1):
+            R = R + Ch[r, t][:, :, None] * dy[r, t][:, None, :]
+            dCh[r, t] = (states[t - a + 1] * dy[r, t][:, None, :]).sum(2)
+            Rx, RB = (R * x[r, t][:, None, :]).sum(2), (R * Bh[r, t][:, :, None]).sum(1)
+            dBh[r, t], dx[r, t] = d[r, t][:, None] * Rx, d[r, t][:, None] * RB
+            direct[r, t] = (Rx * Bh[r, t]).sum(1)
+            decay = torch.exp(d[r, t] * A)
+            dl[r, t] = decay * (R * states[t - a]).sum((1, 2))
+            R = decay[:, None, None] * R
+        dh0[n] = R
+    dd = (direct + dl * A) * (torch.sigmoid(raw) if softplus else 1)
+    shape = (*B.shape[:3], H // G, B.shape[3])
+    return dict(dx=dx if D is None else dx + f64(D)[:, None] * dy, ddt=dd, dA_log=(dl * d * A).sum((0, 1)),
+                dB=dBh.reshape(shape).sum(3), dC=dCh.reshape(shape).sum(3), dD=(dy * x).sum((0, 1, 3)),
+                ddt_bias=dd.sum((0, 1)), dh0=dh0, dl=dl, direct=direct)

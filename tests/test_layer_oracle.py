@@ -56,3 +56,39 @@ def test_e4m3_values_are_torch_codes():
     codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
     codes = codes[~codes.isnan()].unique()
     assert torch.equal(codes, lo.e4m3_values())
+
+
+def test_ssm_by_hand():
+    # one head, one state row, one channel; step 1 and A = -ln 2: S halves, then takes B x
+    x, dt = torch.tensor([8.0, 4.0, 2.0]).view(1, 3, 1, 1), torch.ones(1, 3, 1)
+    B, C = torch.tensor([1.0, 2.0, 3.0]).view(1, 3, 1, 1), torch.tensor([1.0, 1.0, 10.0]).view(1, 3, 1, 1)
+    A_log = torch.log(torch.log(torch.tensor([2.0], dtype=torch.float64)))
+    y, last = lo.ssm(x, dt, A_log, B, C, D=torch.tensor([0.5]), h0=torch.full((1, 1, 1, 1), 16.0))
+    # S: 16/2 + 8 = 16; 8 + 8 = 16; 8 + 6 = 14
+    assert torch.allclose(y.flatten(), torch.tensor([16 + 4.0, 16 + 2.0, 140 + 1.0], dtype=torch.float64), atol=1e-12, rtol=0)
+    assert abs(last.item() - 14) < 1e-12
+    y, last = lo.ssm(x, dt, A_log, B, C, cu=[0, 0, 1, 3])
+    assert torch.allclose(y.flatten(), torch.tensor([8.0, 8.0, 100.0], dtype=torch.float64), atol=1e-12, rtol=0)
+    assert torch.allclose(last.flatten(), torch.tensor([0.0, 8.0, 10.0], dtype=torch.float64), atol=1e-12, rtol=0)
+
+
+@pytest.mark.parametrize("softplus", [False, True])
+@pytest.mark.parametrize("cu", [None, [0, 3, 3, 4, 9]])
+def test_ssm_gradients_by_differences(softplus, cu):
+    nb, T, H, G, N, P = (2, 6, 4, 2, 3, 5) if cu is None else (1, 9, 4, 2, 3, 5)
+    n = nb if cu is None else len(cu) - 1
+    at = dict(x=rand(nb, T, H, P, seed=1), dt=rand(nb, T, H, seed=2).abs() * 0.3, A_log=rand(H, seed=3) * 0.3,
+              B=rand(nb, T, G, N, seed=4), C=rand(nb, T, G, N, seed=5), D=rand(H, seed=6), dt_bias=rand(H, seed=7) * 0.1,
+              h0=rand(n, H, N, P, seed=8))
+    dy, dht = rand(nb, T, H, P, seed=9), rand(n, H, N, P, seed=10)
+    got = lo.ssm_bwd(at["x"], at["dt"], at["A_log"], at["B"], at["C"], dy, dht, at["D"], at["dt_bias"], softplus, at["h0"], cu)
+
+    def loss(v):
+        y, last = lo.ssm(v["x"], v["dt"], v["A_log"], v["B"], v["C"], v["D"], v["dt_bias"], softplus, v["h0"], cu)
+        return (y * dy).sum() + (last * dht).sum()
+
+    for k in at:
+        way, step = rand(*at[k].shape, seed=11), 1e-6
+        diff = (loss(dict(at, **{k: at[k] + step * way})) - loss(dict(at, **{k: at[k] - step * way}))) / (2 * step)
+        mine = (got["d" + k] * way).sum()
+        assert abs(diff - mine) <= 1e-6 * (1 + abs(diff)), (k, diff.item(), mine.item())
