@@ -52,7 +52,7 @@ struct SsmParams {
     int32_t L, total_chunks, seg, total_segs, max_segs;  // max_segs: of one sequence
     int32_t x_bf16, dt_bf16, softplus;
     int32_t num_slots;
-    int32_t split;                 // backward: parts of a group's heads, each with its own sums for dB, dC
+    int32_t split;                 // backward: parts of a group's heads (two to a part), each with its own sums for dB, dC
     int64_t tokens;                // B * T
     int64_t x_stride, dt_stride, b_stride, c_stride;
     const void *x, *dt, *Bm, *C, *dy;
@@ -62,14 +62,16 @@ struct SsmParams {
     void *y, *dx, *ddt, *dB, *dC;
     float *ht, *dh0, *dA_log, *dD, *ddt_bias, *state;
     // workspace
-    int4 *chunk;                   // [total_chunks] first token, length, sequence
-    float *d, *ch, *cl, *fs, *fe;  // [total_chunks][H][L]: see ssm_prep_kernel
-    float *dec;                    // [total_chunks][H] the chunk's whole decay
-    void *S[2], *R[2];             // [total_chunks][H] states in fragment order, high and low parts
-    float *seg_end;                // [2][total_segs][H] N * P each: states of segments from zero
+    float *d, *ch, *cl;            // [total_chunks][H][L]: see ssm_prep_kernel
+    float *seg_state;              // [2][total_segs][H][N][P]: ends of segments from zero, then their starts
     float *seg_dec;                // [2][total_segs][H]
-    float *sums;                   // backward: [total_chunks][H][4] terms of dA_log, ddt_bias, dD
-    float *dBp, *dCp;              // backward: [split][tokens][G][N] where split > 1
+    // backward, for the gradients of steps and decays (kda_layer_ssm_bwd.hip)
+    float *last_state;             // [NS][H][N][P]
+    float *w_rows, *w_cols, *w_diag, *w_qdiag, *w_decay;  // [total_chunks][H][L], w_decay without [L]
+    float *w_o, *w_q;              // [total_chunks][H][N / 16][L]
+    float *w_dot;                  // [total_segs][H][N / 16]
+    float *sums;                   // [total_chunks][H][4] terms of dA_log, ddt_bias, dD
+    float *dBp, *dCp;              // [split][tokens][G][N] where split > 1
 };
 
 size_t ssm_workspace(SsmParams &p, void *ws, bool backward);  // sizes (and, with ws, binds) the workspace

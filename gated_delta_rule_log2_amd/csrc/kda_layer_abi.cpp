@@ -68,8 +68,8 @@ kda_status check_norm(const kda_norm_desc *d, bool fp8, NormParams &p) {
     return KDA_OK;
 }
 
+constexpr int64_t kMaxStride = 1 << 24;  // a chunk's offsets stay in 32 bits
 constexpr int64_t kCarryGroups = 512;  // workgroups wanted of a pass over chunks: two for each CU
-constexpr int64_t kBwdGroups = 512;    // and of the backward's chunk kernel
 
 kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {
     if (!d) return KDA_ERR_NULL_POINTER;
@@ -80,6 +80,7 @@ kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {
     if (d->x_stride < (int64_t)d->H * d->P || d->dt_stride < d->H || d->b_stride < (int64_t)d->G * d->N ||
         d->c_stride < (int64_t)d->G * d->N)
         return KDA_ERR_SHAPE;
+    if ((int64_t)d->H * d->P > kMaxStride || (int64_t)d->G * d->N > kMaxStride || d->x_stride > kMaxStride || d->b_stride > kMaxStride || d->c_stride > kMaxStride) return KDA_ERR_SHAPE;
     const kda_status st = check_seqs(d->B, d->T, d->num_seqs, d->cu_seqlens_host);
     if (st != KDA_OK) return st;
     if (!dtype_ok(d->x_dtype) || !dtype_ok(d->dt_dtype)) return KDA_ERR_DTYPE;
@@ -96,7 +97,7 @@ kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {
 
 // The chunks, and how many of them make a segment: enough segments that the passes over chunks
 // fill the GPU, and at least four chunks in each (joining a segment costs about one).
-kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p, bool backward) {
+kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p) {
     auto each = [&](auto f) {
         if (d->cu_seqlens_host)
             for (int32_t n = 0; n < p.NS; ++n) f((d->cu_seqlens_host[n + 1] - d->cu_seqlens_host[n] + p.L - 1) / p.L, 1);
@@ -104,23 +105,17 @@ kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p, bool backward) {
     };
     int64_t chunks = 0, segs = 0, most = 1;
     each([&](int64_t c, int64_t times) { chunks += c * times; });
-    const int64_t tiles = ((backward ? p.N : p.P) + 63) / 64;
     if (chunks * p.H > INT32_MAX) return KDA_ERR_SHAPE;
-    const int64_t seg = (chunks * p.H * tiles + kCarryGroups - 1) / kCarryGroups;
+    const int64_t seg = (chunks * p.H + kCarryGroups - 1) / kCarryGroups;
     p.seg = (int32_t)(seg < 4 ? 4 : seg);
     each([&](int64_t c, int64_t times) {
         const int64_t s = c > p.seg ? (c + p.seg - 1) / p.seg : 1;
         segs += s * times;
         if (s > most) most = s;
     });
-    if (segs * p.H * tiles * 2 > INT32_MAX - 8) return KDA_ERR_SHAPE;
+    if (segs * p.H * 8 > INT32_MAX - 8) return KDA_ERR_SHAPE;
     p.total_chunks = (int32_t)chunks; p.total_segs = (int32_t)segs; p.max_segs = (int32_t)most;
-    const int32_t hg = p.H / p.G;
-    const int64_t groups = chunks * p.G > 0 ? chunks * p.G : 1;
-    int64_t split = groups < kBwdGroups ? (kBwdGroups + groups - 1) / groups : 1;
-    if (split > hg) split = hg;
-    const int32_t per = (int32_t)((hg + split - 1) / split);
-    p.split = (hg + per - 1) / per;
+    p.split = (p.H / p.G + 1) / 2;  // two heads to a workgroup of dC's and dB's scans
     return KDA_OK;
 }
 
@@ -133,24 +128,27 @@ size_t ssm_workspace(SsmParams &p, void *ws, bool backward) {
         off += (bytes + 255) / 256 * 256;
         return static_cast<void *>(at);
     };
-    const size_t ch = (size_t)p.total_chunks * p.H, tok = ch * p.L * sizeof(float), eb = p.x_bf16 ? 2 : 4;
+    const size_t ch = (size_t)p.total_chunks * p.H, tok = ch * p.L * sizeof(float);
     const size_t state = (size_t)p.N * p.P, dirs = backward ? 2 : 1;
-    p.chunk = static_cast<int4 *>(take((size_t)p.total_chunks * sizeof(int4)));
     p.d = static_cast<float *>(take(tok));
     p.ch = static_cast<float *>(take(tok));
     p.cl = static_cast<float *>(take(tok));
-    p.fs = static_cast<float *>(take(tok));
-    p.fe = static_cast<float *>(take(tok));
-    p.dec = static_cast<float *>(take(ch * sizeof(float)));
-    const int parts = backward && p.x_bf16 ? 2 : 1;
-    for (int i = 0; i < parts; ++i) p.S[i] = take(ch * state * eb);
-    for (int i = 0; backward && i < parts; ++i) p.R[i] = take(ch * state * eb);
+    auto floats = [&](size_t n) { return static_cast<float *>(take(n * sizeof(float))); };
     if (p.max_segs > 1) {
-        p.seg_end = static_cast<float *>(take(dirs * p.total_segs * p.H * state * sizeof(float)));
-        p.seg_dec = static_cast<float *>(take(dirs * p.total_segs * p.H * sizeof(float)));
+        p.seg_state = floats(dirs * p.total_segs * p.H * state);
+        p.seg_dec = floats(dirs * p.total_segs * p.H);
     }
     if (backward) {
-        p.sums = static_cast<float *>(take(ch * 4 * sizeof(float)));
+        p.last_state = floats((size_t)p.NS * p.H * state);
+        p.w_rows = floats(ch * p.L);
+        p.w_cols = floats(ch * p.L);
+        p.w_diag = floats(ch * p.L);
+        p.w_qdiag = floats(ch * p.L);
+        p.w_decay = floats(ch);
+        p.w_o = floats(ch * p.L * (p.N / 16));
+        p.w_q = floats(ch * p.L * (p.N / 16));
+        p.w_dot = floats((size_t)p.total_segs * p.H * (p.N / 16));
+        p.sums = floats(ch * 4);
         if (p.split > 1) {
             const size_t part = (size_t)p.split * p.tokens * p.G * p.N * sizeof(float);
             p.dBp = static_cast<float *>(take(part));
@@ -164,14 +162,14 @@ size_t ssm_workspace(SsmParams &p, void *ws, bool backward) {
 
 using namespace kda;
 
-static kda_status ssm_prepare(const kda_ssm_desc *d, SsmParams &p, bool backward) {
+static kda_status ssm_prepare(const kda_ssm_desc *d, SsmParams &p) {
     const kda_status st = check_ssm(d, p);
-    return st == KDA_OK ? plan_ssm(d, p, backward) : st;
+    return st == KDA_OK ? plan_ssm(d, p) : st;
 }
 
 static kda_status ssm_size(const kda_ssm_desc *d, size_t *bytes, bool backward) {
     SsmParams p;
-    const kda_status st = ssm_prepare(d, p, backward);
+    const kda_status st = ssm_prepare(d, p);
     if (st != KDA_OK) return st;
     if (!bytes) return KDA_ERR_NULL_POINTER;
     *bytes = ssm_workspace(p, nullptr, backward);
@@ -287,7 +285,7 @@ kda_status kda_ssm_fwd(const kda_ssm_desc *d, const void *x, const void *dt, con
                        const int64_t *cu_seqlens, void *y, float *final_state, void *workspace,
                        size_t workspace_bytes, hipStream_t stream) {
     SsmParams p;
-    const kda_status st = ssm_prepare(d, p, false);
+    const kda_status st = ssm_prepare(d, p);
     if (st != KDA_OK) return st;
     if (p.tokens > 0 && (!x || !dt || !Bm || !C || !y)) return KDA_ERR_NULL_POINTER;
     if (!A_log) return KDA_ERR_MISSING_A_LOG;
@@ -305,7 +303,7 @@ kda_status kda_ssm_bwd(const kda_ssm_desc *d, const void *x, const void *dt, con
                        float *dA_log, void *dB, void *dC, float *dD, float *ddt_bias, float *dh0, void *workspace,
                        size_t workspace_bytes, hipStream_t stream) {
     SsmParams p;
-    const kda_status st = ssm_prepare(d, p, true);
+    const kda_status st = ssm_prepare(d, p);
     if (st != KDA_OK) return st;
     if (p.tokens > 0 && (!x || !dt || !Bm || !C || !dy || !dx || !ddt || !dB || !dC)) return KDA_ERR_NULL_POINTER;
     if (!dA_log) return KDA_ERR_NULL_POINTER;

@@ -12,6 +12,13 @@ namespace kda {
 // accesses, which gfx950 serves at every address.
 struct Raw16 { uint32_t w[4]; };
 
+// Two values rounded to bf16 by one instruction (two single conversions cost a third to join).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+
 template <typename T> struct Vec8;
 template <> struct Vec8<uint16_t> {
     Raw16 r;
@@ -26,7 +33,7 @@ template <> struct Vec8<uint16_t> {
     }
     __device__ __forceinline__ void set(const float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r.w[i] = (uint32_t)f2bf(x[2 * i]) | ((uint32_t)f2bf(x[2 * i + 1]) << 16);
+        for (int i = 0; i < 4; ++i) r.w[i] = pack_bf(x[2 * i], x[2 * i + 1]);
     }
     __device__ __forceinline__ void store(uint16_t *p) const { __builtin_memcpy(p, &r, 16); }
     __device__ __forceinline__ void part(const uint16_t *p, int n) {  // n < 8 elements, the others 0

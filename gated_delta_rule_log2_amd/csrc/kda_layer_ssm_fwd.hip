@@ -1,5 +1,5 @@
-// kda_layer_ssm_fwd.hip -- the state space scan: chunk preparation, the chunk outputs and the
-// single-token step (the pass over chunks is in kda_layer_ssm.h, with the formulas).
+// kda_layer_ssm_fwd.hip -- the state space scan: preparation, joining of segments, the
+// forward's scan and the single-token step (the scan itself is in kda_layer_ssm.h).
 #include "kda_layer_ssm.h"
 
 namespace kda {
@@ -11,177 +11,100 @@ __device__ __forceinline__ float step_of(float raw, int softplus) {
     return softplus ? fmaxf(raw, 0.f) + log1pf(expf(-fabsf(raw))) : raw;
 }
 
-// For each token of a chunk and head, [chunk][head][L]:
-//   d   the step;  ch + cl  the sum of log2 decays up to the token, in two floats (the sums
-//   run in 64 bits: differences of near tokens keep fp32 precision however long the chunk's
-//   decay is);  fs = d e^{cum_L - cum};  fe = e^{cum};  and dec = e^{cum_L}.
-// Tokens past the chunk's end have d = fs = 0 and the last token's sum.  A token's log2 decay
-// is held to -200, where 2^x is 0 in fp32, so that sums stay finite.
-// One workgroup per chunk and 64 heads: dt comes in rows of heads and leaves in rows of tokens.
+// For each token of a chunk and head, [chunk][head][L]: the step d, and the sum of log2 decays
+// up to the token, ch + cl, in two floats (the sums run in 64 bits: differences of near tokens
+// keep fp32 precision however large the chunk's whole decay is).  Tokens past the chunk's end
+// have d = 0 and the last token's sum.  A token's log2 decay is held to -200, where 2^x is 0 in
+// fp32, so that sums stay finite.
+// One workgroup per chunk and eight heads, a wave for two of them, a lane for a token.
+constexpr int kPrepHeads = 8;
 __global__ void __launch_bounds__(256) ssm_prep_kernel(SsmParams p, int hblocks) {
-    __shared__ float raw[64][65];
-    const int c = blockIdx.x / hblocks, h0 = (blockIdx.x % hblocks) * 64;
+    const int c = blockIdx.x / hblocks, h0 = (blockIdx.x % hblocks) * kPrepHeads;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const Unit u = locate<256, false>(p, c);
     const SeqSpan q = seq_span(p, u.n);
     const int64_t tok0 = q.first + (int64_t)u.local * p.L;
     const int len = u.chunks == 0 ? 0 : (int)(q.end - tok0 < p.L ? q.end - tok0 : p.L);
-    if (threadIdx.x == 0 && h0 == 0) p.chunk[c] = make_int4((int)tok0, len, u.n, u.local);
-    for (int e = threadIdx.x; e < p.L * 64; e += 256) {
-        const int row = e >> 6, h = h0 + (e & 63);
-        raw[row][e & 63] = row < len && h < p.H ? load_f32(p.dt, (tok0 + row) * p.dt_stride + h, p.dt_bf16) : 0.f;
-    }
-    __syncthreads();
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    for (int k = 0; k < 16; ++k) {
-        const int h = h0 + 16 * w + k;
-        if (h >= p.H) break;
-        const bool in = lane < len;
-        const float d = in ? step_of(raw[lane < p.L ? lane : 0][16 * w + k] + (p.dt_bias ? p.dt_bias[h] : 0.f), p.softplus) : 0.f;
-        double a = -exp((double)p.A_log[h]) * 1.4426950408889634 * (double)d;
-        if (a < -200.) a = -200.;
-        if (!in) a = 0.;
+    constexpr int K = kPrepHeads / 4;
+    float raw[K];
+    double a[K];
+    const bool in = lane < len;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double b = __shfl_up(a, o, 64);
-            if (lane >= o) a += b;
+    for (int k = 0; k < K; ++k) {
+        const int h = h0 + K * w + k;
+        raw[k] = in && h < p.H ? load_f32(p.dt, (tok0 + lane) * p.dt_stride + h, p.dt_bf16) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int h = h0 + K * w + k < p.H ? h0 + K * w + k : p.H - 1;
+        raw[k] = in ? step_of(raw[k] + (p.dt_bias ? p.dt_bias[h] : 0.f), p.softplus) : 0.f;
+        a[k] = -exp((double)p.A_log[h]) * 1.4426950408889634 * (double)raw[k];
+        if (a[k] < -200.) a[k] = -200.;
+        if (!in) a[k] = 0.;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const double b = __shfl_up(a[k], o, 64);
+            if (lane >= o) a[k] += b;
         }
-        const double whole = __shfl(a, 63, 64);
-        if (lane < p.L) {
-            const size_t i = ((size_t)c * p.H + h) * p.L + lane;
-            const float hi = (float)a;
-            p.d[i] = d;
-            p.ch[i] = hi;
-            p.cl[i] = (float)(a - (double)hi);
-            p.fs[i] = d * __builtin_amdgcn_exp2f((float)(whole - a));
-            p.fe[i] = __builtin_amdgcn_exp2f(hi);
-        }
-        if (lane == 0) p.dec[(size_t)c * p.H + h] = __builtin_amdgcn_exp2f((float)whole);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int h = h0 + K * w + k;
+        if (h >= p.H || lane >= p.L) continue;
+        const size_t i = ((size_t)c * p.H + h) * p.L + lane;
+        const float hi = (float)a[k];
+        p.d[i] = raw[k];
+        p.ch[i] = hi;
+        p.cl[i] = (float)(a[k] - (double)hi);
     }
 }
 
-template <typename T> struct OutLds {
-    static constexpr int L = ChunkLen<T>::value, PAD = sizeof(T) == 2 ? 8 : 4, XPAD = sizeof(T) == 2 ? 16 : 4;
-    static constexpr int LD = 128 + PAD, XLD = 128 + XPAD, MLD = L + PAD;
-    T c[L * LD];
-    T b[L * LD];  // B, then the masked products M
-    T x[L * XLD];
-    float d[L], ch[L], cl[L], fe[L];
-};
-
-// y of one chunk and head.  Four waves: first the products B_j . C_i of the 16x16 blocks at or
-// below the diagonal, dealt to the waves in turn, whose accumulators (a lane has one i and four
-// j) become M_ij = (C_i . B_j) e^{cum_i - cum_j} d_j in LDS; then a wave takes 32 columns of y
-// (all i, or a share of them where P is small) and adds x^T M^T and, scaled by e^{cum_i}, S0^T C^T,
-// whose S0 comes as fragments straight from memory.  Rows of the products are columns of y, so a
-// lane ends with eight consecutive values of one token.
-template <typename T>
-__global__ void __launch_bounds__(256) ssm_out_kernel(SsmParams p) {
-    using M = OutLds<T>;
-    constexpr int L = M::L, IT = L / 16;
-    __shared__ M lds;
-    const int64_t b = xcd_order();
-    if (b >= (int64_t)p.total_chunks * p.H) return;
-    const int h = (int)(b % p.H), c = (int)(b / p.H);
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, r = lane & 15;
-    const int4 ci = p.chunk[c];
-    const int64_t tok0 = ci.x;
-    const int len = ci.y, grp = h / (p.H / p.G), n8 = p.N / 8, x8 = p.P / 8;
-    {
-        Tile<T, L, 16, 256> tb, tc, tx;
-        tb.request(static_cast<const T *>(p.Bm) + tok0 * p.b_stride + (int64_t)grp * p.N, p.b_stride, n8, len);
-        tc.request(static_cast<const T *>(p.C) + tok0 * p.c_stride + (int64_t)grp * p.N, p.c_stride, n8, len);
-        tx.request(static_cast<const T *>(p.x) + tok0 * p.x_stride + (int64_t)h * p.P, p.x_stride, x8, len);
-        const size_t i = ((size_t)c * p.H + h) * L;
-        for (int k = tid; k < 4 * L; k += 256) {
-            const float *from = k < L ? p.d : k < 2 * L ? p.ch : k < 3 * L ? p.cl : p.fe;
-            float *to = k < L ? lds.d : k < 2 * L ? lds.ch : k < 3 * L ? lds.cl : lds.fe;
-            to[k % L] = from[i + k % L];
-        }
-        tb.put(lds.b, M::LD, n8);
-        tc.put(lds.c, M::LD, n8);
-        tx.put(lds.x, M::XLD, x8);
+// The first states of segments from their ends: in place, seg_state[seg] becomes the state that
+// reaches the segment, from the sequence's (or dht) on.  Four values to a thread; the next
+// segment's end is requested before this one's start is stored.
+__global__ void __launch_bounds__(256) ssm_join_kernel(SsmParams p) {
+    const int state = p.N * p.P, blocks = state / 1024 > 0 ? state / 1024 : 1;
+    int64_t b = blockIdx.x;
+    const int e4 = ((int)(b % blocks) * 256 + threadIdx.x) * 4;
+    b /= blocks;
+    const int h = (int)(b % p.H);
+    b /= p.H;
+    const int n = (int)(b % p.NS);
+    const bool rev = b / p.NS;
+    // the sequence's first segment and their number
+    __shared__ int before[4];
+    int seg0 = 0, segs;
+    auto count = [&](int m) {
+        const SeqSpan q = seq_span(p, m);
+        const int chunks = (int)((q.end - q.first + p.L - 1) / p.L);
+        return chunks > p.seg ? (chunks + p.seg - 1) / p.seg : 1;
+    };
+    segs = count(n);
+    if (!p.cu_seqlens) {
+        seg0 = n * segs;
+    } else {
+        int s = 0;
+        for (int m = threadIdx.x; m < n; m += 256) s += count(m);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+        if ((threadIdx.x & 63) == 0) before[threadIdx.x >> 6] = s;
+        __syncthreads();
+        seg0 = before[0] + before[1] + before[2] + before[3];
     }
-    __syncthreads();
-    constexpr int BLOCKS = IT == 4 ? 12 : 4, MAXB = BLOCKS / 4;
-    f32x4 gm[MAXB];
-    T *m = lds.b;
-#pragma unroll
-    for (int k = 0; k < MAXB; ++k) {
-        int it, jt;
-        causal_block(w + 4 * k, it, jt);
-        f32x4 acc = zero4();
-        if (jt <= it) {
-            for (int nb = 0; nb < p.N; nb += 32)
-                acc = mma(acc, row_frag<false>(lds.b + (16 * jt + r) * M::LD + nb, g),
-                          row_frag<false>(lds.c + (16 * it + r) * M::LD + nb, g));
-            const int i = 16 * it + r;
-            const float hi = lds.ch[i], lo = lds.cl[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 16 * jt + 4 * g + e;
-                const float decay = __builtin_amdgcn_exp2f((hi - lds.ch[j]) + (lo - lds.cl[j]));
-                acc[e] = j <= i ? acc[e] * (decay * lds.d[j]) : 0.f;
-            }
-        }
-        gm[k] = acc;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < MAXB; ++k) {
-        int it, jt;
-        causal_block(w + 4 * k, it, jt);
-        store4(m + (16 * it + r) * M::MLD + 16 * jt + 4 * g, gm[k][0], gm[k][1], gm[k][2], gm[k][3]);
-    }
-    __syncthreads();
-
-    const int pblocks = p.P / 32, split = pblocks == 1 ? 4 : pblocks == 2 ? 2 : 1;
-    const int pb = w / split, its = (IT + split - 1) / split, it0 = (w % split) * its;
-    if (pb >= pblocks) return;
-    const T *S0 = static_cast<const T *>(p.S[0]) + ((size_t)c * p.H + h) * p.N * p.P;
-    const float D = p.D ? p.D[h] : 0.f;
-    f32x4 am[2][IT], as[2][IT];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int q = 0; q < IT; ++q) am[t][q] = as[t][q] = zero4();
-#pragma unroll
-    for (int kb = 0; kb < L / 32; ++kb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const Frag<T> fx = col_frag<false, true>(lds.x + 32 * kb * M::XLD, M::XLD, 32 * pb + 4 * t, r, g);
-#pragma unroll
-            for (int q = 0; q < IT; ++q) {
-                const int it = it0 + q;
-                if (q < its && it < IT && it >= 2 * kb)
-                    am[t][q] = mma(am[t][q], fx, row_frag<false>(m + (16 * it + r) * M::MLD + 32 * kb, g));
-            }
-        }
-    for (int nb = 0; nb < p.N / 32; ++nb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const Frag<T> fs = load_frag(S0 + ((size_t)nb * (p.P / 16) + 2 * pb + t) * 512 + lane * 8);
-#pragma unroll
-            for (int q = 0; q < IT; ++q) {
-                const int it = it0 + q;
-                if (q < its && it < IT)
-                    as[t][q] = mma(as[t][q], fs, row_frag<true>(lds.c + (16 * it + r) * M::LD + 32 * nb, g));
-            }
-        }
-    T *y = static_cast<T *>(p.y) + (tok0 * p.H + h) * p.P + 32 * pb + 8 * g;
-#pragma unroll
-    for (int q = 0; q < IT; ++q) {
-        const int i = 16 * (it0 + q) + r;
-        if (q >= its || it0 + q >= IT || i >= len) continue;
-        float xv[8], o[8];
-        Vec8<T> vx;
-        __builtin_memcpy(&vx, lds.x + i * M::XLD + 32 * pb + 8 * g, sizeof(vx));
-        vx.get(xv);
-        const float fe = lds.fe[i];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[4 * t + e] = am[t][q][e] + fe * as[t][q][e] + D * xv[4 * t + e];
-        store8(y + (int64_t)i * p.H * p.P, o);
+    if (seg0 + segs > p.total_segs) return;  // only where the device's offsets are not the host's
+    if (e4 >= state) return;
+    const float *init = rev ? p.dht : p.h0;
+    f32x4 run = zero4(), next = zero4();
+    if (init) run = *reinterpret_cast<const f32x4 *>(init + ((size_t)n * p.H + h) * state + e4);
+    auto at = [&](int s) { return (size_t)((rev ? p.total_segs + seg0 + segs - 1 - s : seg0 + s)) * p.H + h; };
+    if (segs > 1) next = *reinterpret_cast<const f32x4 *>(p.seg_state + at(0) * state + e4);
+    for (int s = 0; s < segs; ++s) {
+        const f32x4 end = next;
+        if (s + 2 < segs) next = *reinterpret_cast<const f32x4 *>(p.seg_state + at(s + 1) * state + e4);
+        *reinterpret_cast<f32x4 *>(p.seg_state + at(s) * state + e4) = run;
+        if (s + 1 < segs) run = run * p.seg_dec[at(s)] + end;
     }
 }
 
@@ -258,14 +181,6 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
     }
 }
 
-template <typename T> hipError_t fwd(const SsmParams &p, hipStream_t s) {
-    hipError_t e = launch_ssm_prep(p, s);
-    if (e == hipSuccess) e = launch_carry<T, false, false>(p, false, s);
-    if (e != hipSuccess || p.total_chunks == 0) return e;
-    hipLaunchKernelGGL(ssm_out_kernel<T>, dim3(xcd_grid((int64_t)p.total_chunks * p.H)), dim3(256), 0, s, p);
-    return hipGetLastError();
-}
-
 template <typename T> hipError_t step(const SsmParams &p, hipStream_t s) {
     // narrow tiles where whole heads would leave CUs idle
     const bool narrow = (int64_t)p.B * p.H * ((p.P + 127) / 128) < 512;
@@ -281,12 +196,27 @@ template <typename T> hipError_t step(const SsmParams &p, hipStream_t s) {
 
 hipError_t launch_ssm_prep(const SsmParams &p, hipStream_t s) {
     if (p.total_chunks == 0) return hipSuccess;
-    const int hblocks = (p.H + 63) / 64;
+    const int hblocks = (p.H + kPrepHeads - 1) / kPrepHeads;
     const int64_t grid = (int64_t)p.total_chunks * hblocks;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL(ssm_prep_kernel, dim3((unsigned)grid), dim3(256), 0, s, p, hblocks);
     return hipGetLastError();
 }
+
+hipError_t launch_ssm_join(const SsmParams &p, int dirs, hipStream_t s) {
+    const int64_t state = (int64_t)p.N * p.P, blocks = state / 1024 > 0 ? state / 1024 : 1;
+    const int64_t grid = (int64_t)dirs * p.NS * p.H * blocks;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)grid), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+namespace {
+template <typename T> hipError_t fwd(const SsmParams &p, hipStream_t s) {
+    const hipError_t e = launch_segments<T>(p, 1, s);
+    return e == hipSuccess ? launch_scan<T, kY>(p, 1, s) : e;
+}
+}  // namespace
 
 hipError_t launch_ssm_fwd(const SsmParams &p, hipStream_t s) { return p.x_bf16 ? fwd<uint16_t>(p, s) : fwd<float>(p, s); }
 hipError_t launch_ssm_step(const SsmParams &p, hipStream_t s) { return p.x_bf16 ? step<uint16_t>(p, s) : step<float>(p, s); }

@@ -210,7 +210,7 @@ def test_ssm_workspace_covers_every_split(lib):
         n = ctypes.c_size_t(0)
         assert lib.kda_ssm_bwd_workspace_size(ctypes.byref(ssm_desc(T=T)), ctypes.byref(n)) == 0
         sizes.append(n.value)
-    assert sizes == sorted(sizes) and sizes[-1] > (1 << 14) * 4 * 64 * 64 * 8
+    assert sizes == sorted(sizes) and sizes[-1] > (1 << 20) * 4 * 4 * 7  # seven fp32 values a token and head at least
     n = ctypes.c_size_t(0)
     huge = ssm_desc(T=1 << 30, H=1 << 12, x_stride=1 << 18, dt_stride=1 << 12)
     assert lib.kda_ssm_bwd_workspace_size(ctypes.byref(huge), ctypes.byref(n)) == S["KDA_ERR_SHAPE"]
