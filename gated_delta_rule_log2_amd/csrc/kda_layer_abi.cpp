@@ -68,7 +68,7 @@ kda_status check_norm(const kda_norm_desc *d, bool fp8, NormParams &p) {
     return KDA_OK;
 }
 
-constexpr int64_t kMaxStride = 1 << 24;  // a chunk's offsets stay in 32 bits
+constexpr int64_t kMaxStride = (1 << 24) - 1;  // a chunk's offsets stay in 32 bits
 constexpr int64_t kCarryGroups = 512;  // workgroups wanted of a pass over chunks: two for each CU
 
 kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {

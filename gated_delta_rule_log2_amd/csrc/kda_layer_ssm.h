@@ -260,20 +260,17 @@ template <typename T, int L, int W> struct Tile {
     static constexpr int W8 = W / 8, STEP = 256 / W8, K = L / STEP;
     Vec8<T> v[K];
     int len, cols;
+    // One sequence of loads for full and partial tiles: behind a branch each tile's loads would wait
+    // for the one's before.
     __device__ __forceinline__ void request(const T *base, int stride, int columns, int length) {
-        const int row = threadIdx.x / W8, c = 8 * (threadIdx.x % W8);
+        const unsigned row = threadIdx.x / W8, c = 8 * (threadIdx.x % W8);
         len = length;
         cols = columns;
-        if (len == L && cols == W) {
-            const unsigned off = row * stride + c;
+        const unsigned at = (int)c < cols ? c : 0;
 #pragma unroll
-            for (int k = 0; k < K; ++k) v[k].load(behind(base + (int64_t)k * STEP * stride, off));
-        } else if (len > 0) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int at = row + k * STEP < len ? row + k * STEP : len - 1;
-                v[k].load(behind(base, at * stride + (c < cols ? c : 0)));
-            }
+        for (int k = 0; k < K; ++k) {
+            const unsigned from = row + k * STEP < (unsigned)len ? row + k * STEP : len - 1;
+            v[k].load(behind(base, __umul24(from, stride) + at));
         }
     }
     __device__ __forceinline__ void put(T *lds) {
@@ -368,7 +365,7 @@ template <typename T, int KW, int CT, int MODE> struct ScanLds {
     T key[L * Layout<T, KW>::LD], val[L * Layout<T, VW>::LD];
     T q[MODE == kFirst ? 4 : L * Layout<T, KW>::LD];
     T m[MODE == kFirst ? 4 : L * Layout<T, 64>::LD];
-    T x[MODE == kDx ? L * Layout<T, VW>::LD : 4];
+    T other[MODE == kDx || scan_sums(MODE) ? L * Layout<T, VW>::LD : 4];  // x; or C, B for dC, dB
     float tok[5][L];
     float rows[MODE == kDx ? 4 : 1][L], cols[MODE == kDx ? 4 : 1][L], diag[L], qdiag[L];
     float wave[4], dec;
@@ -466,7 +463,7 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
     const T *Bm = static_cast<const T *>(p.Bm) + (int64_t)grp * p.N, *Cm = static_cast<const T *>(p.C) + (int64_t)grp * p.N;
     const int xs = (int)p.x_stride, bs = (int)p.b_stride, cs = (int)p.c_stride, ys = p.H * p.P;
     Tile<T, L, KW> tk, tq;
-    Tile<T, L, VW> tv, tx;
+    Tile<T, L, VW> tv, to;
     Tokens<L> tt;
     auto chunk_at = [&](int k) { return sg.first + (rev ? sg.count - 1 - k : k); };
     const float D = !SUMS && OUT && p.D ? p.D[h0] : 0.f;
@@ -479,21 +476,32 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
         const T *bt = Bm + t0 * bs, *ct = Cm + t0 * cs;
         if constexpr (MODE == kY) {
             tk.request(bt, bs, KD, len);
-            tq.request(ct, cs, KD, len);
             tv.request(xt + v0, xs, vcols, len);
         } else if constexpr (MODE == kDx) {
             tk.request(ct, cs, KD, len);
-            tq.request(bt, bs, KD, len);
             tv.request(yt + v0, ys, vcols, len);
-            tx.request(xt + v0, xs, vcols, len);
+            to.request(xt + v0, xs, vcols, len);
         } else {
             tk.request(rev ? yt : xt, rev ? ys : xs, KD, len);
-            if constexpr (OUT) tq.request(rev ? xt : yt, rev ? xs : ys, KD, len);
-            if (with_val) tv.request((rev ? ct : bt) + v0, rev ? cs : bs, vcols, len);
+            if (with_val) {
+                tv.request((rev ? ct : bt) + v0, rev ? cs : bs, vcols, len);
+                if constexpr (OUT) to.request((rev ? bt : ct) + v0, rev ? bs : cs, vcols, len);
+            }
         }
         tt.request(p, (size_t)c * p.H + h);
     };
-    if (sg.count > 0) request(chunk_at(0), h0, true);
+    auto request_q = [&](int c, int h) {  // later than the others: its registers are then free of products
+        const int64_t t0 = token_of(c);
+        const int len = length_of(c);
+        if constexpr (MODE == kY) tq.request(Cm + t0 * cs, cs, KD, len);
+        else if constexpr (MODE == kDx) tq.request(Bm + t0 * bs, bs, KD, len);
+        else if constexpr (MODE == kDc) tq.request(dy + t0 * ys + (int64_t)h * p.P, ys, KD, len);
+        else if constexpr (MODE == kDb) tq.request(x + t0 * xs + (int64_t)h * p.P, xs, KD, len);
+    };
+    if (sg.count > 0) {
+        request(chunk_at(0), h0, true);
+        request_q(chunk_at(0), h0);
+    }
     float whole = 1.f;
     for (int k = 0; k < sg.count; ++k) {
         const int c = chunk_at(k), len = length_of(c);
@@ -511,16 +519,9 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
             tk.put(lds.key);
             if constexpr (OUT) tq.put(lds.q);
             if (hh == 0) tv.put(lds.val);
-            if constexpr (MODE == kDx) tx.put(lds.x);
+            if (hh == 0 && OUT && MODE != kY) to.put(lds.other);
             tt.put(lds.tok, lds.dec, rev);
             __syncthreads();
-            float dv[SUMS ? IT : 1][4];  // before the next tiles' loads: they complete in order
-            if constexpr (SUMS)
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const int i = 16 * it + r < len ? 16 * it + r : len - 1;
-                    if (active) load_run(MODE == kDc ? behind(Cm + t0 * cs, i * cs + run0) : behind(Bm + t0 * bs, i * bs + run0), dv[it]);
-                }
             if (hh + 1 < nheads) request(c, h + 1, false);
             else if (k + 1 < sg.count) request(chunk_at(k + 1), h0, true);
 
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
 #pragma unroll
                             for (int vb = 0; vb < VW / 32; ++vb)
                                 dyx = mma(dyx, row_frag<false, VW>(lds.val, 16 * jt + r, 32 * vb, g),
-                                          row_frag<false, VW>(lds.x, a, 32 * vb, g));
+                                          row_frag<false, VW>(lds.other, a, 32 * vb, g));
                         const float hi = lds.tok[1][a], lo = lds.tok[2][a], da = lds.tok[0][a];
                         float ch[4], cl[4], db[4];
                         load_run(&lds.tok[1][b0], ch);
@@ -593,8 +594,8 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
                     if (tid == 0) p.w_decay[chn] = (lds.wave[0] + lds.wave[1]) + (lds.wave[2] + lds.wave[3]);
                 }
             }
+            Frag<T> fv[KS][CT];
             if (active) {
-                Frag<T> fv[KS][CT];
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -650,15 +651,20 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
                         } else {
 #pragma unroll
                             for (int e = 0; e < RUN; ++e) sum[it][e] += o[e];
-                            float dot = 0.f;  // the rows past the end have zq = 0
+                            float dot = 0.f;
+                            load_run(lds.other + Layout<T, VW>::at(i, run0 - v0), v);
 #pragma unroll
-                            for (int e = 0; e < RUN; ++e) dot += real ? dv[it][e] * zq[it][0][e] : 0.f;
+                            for (int e = 0; e < RUN; ++e) dot += v[e] * zq[it][0][e];
                             dot = sum_col_groups(dot);
                             if (g == 0) *behind((MODE == kDc ? p.w_o : p.w_q) + (chn * (p.N / 16) + tile) * L, i) = f * dot;
                         }
                         phase();
                     }
                 }
+            }
+            if (hh + 1 < nheads) request_q(c, h + 1);
+            else if (k + 1 < sg.count) request_q(chunk_at(k + 1), h0);
+            if (active) {
                 const float dec = lds.dec;
                 whole *= dec;
 #pragma unroll
@@ -686,7 +692,7 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
             if (active)
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    const int i = 16 * it + lane_r;
+                    const int i = 16 * it + (fresh(lane_r) & 15);
                     if (i >= len) continue;
                     const int64_t base = (t0 * p.G + grp) * p.N;
                     const int at = i * p.G * p.N + run0;
