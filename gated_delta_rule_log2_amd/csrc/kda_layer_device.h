@@ -5,13 +5,6 @@
 
 namespace kda {
 
-// Eight consecutive channels as fp32, from any element-aligned address.  A row of D
-// channels is cut into ceil(D / 8) vectors; where 8 does not divide D the last vector is
-// moved back to end with the row (vec_channel), so its first channels are also another
-// vector's: both compute the same values.  The copies below let the compiler use 16-byte
-// accesses, which gfx950 serves at every address.
-struct Raw16 { uint32_t w[4]; };
-
 // Two values rounded to bf16 by one instruction (two single conversions cost a third to join).
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -19,80 +12,68 @@ __device__ __forceinline__ uint32_t pack_bf(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-template <typename T> struct Vec8;
-template <> struct Vec8<uint16_t> {
-    Raw16 r;
-    __device__ __forceinline__ void load(const uint16_t *p) { __builtin_memcpy(&r, p, 16); }
-    __device__ __forceinline__ void zero() { r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0; }
-    __device__ __forceinline__ void get(float (&o)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = __uint_as_float(r.w[i] << 16);
-            o[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
-        }
-    }
-    __device__ __forceinline__ void set(const float (&x)[8]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.w[i] = pack_bf(x[2 * i], x[2 * i + 1]);
-    }
-    __device__ __forceinline__ void store(uint16_t *p) const { __builtin_memcpy(p, &r, 16); }
-    __device__ __forceinline__ void part(const uint16_t *p, int n) {  // n < 8 elements, the others 0
-        uint16_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (uint16_t)0;
-        __builtin_memcpy(&r, v, 16);
-    }
-    __device__ __forceinline__ void store_part(uint16_t *p, int n) const {
-        uint16_t v[8];
-        __builtin_memcpy(v, &r, 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = v[i];
-    }
-};
-template <> struct Vec8<float> {
-    Raw16 r[2];
-    __device__ __forceinline__ void load(const float *p) { __builtin_memcpy(r, p, 32); }
+// V consecutive channels as fp32, from any element-aligned address.  A row of D channels is cut
+// into ceil(D / V) vectors; where V does not divide D the last vector is moved back to end with
+// the row (vec_channel), so its first channels are also another vector's: both compute the same
+// values.  The copies below let the compiler use wide accesses, which gfx950 serves at every
+// address.
+template <typename T, int V> struct Vec {
+    uint32_t w[V * sizeof(T) / 4];
+    __device__ __forceinline__ void load(const T *p) { __builtin_memcpy(w, p, sizeof(w)); }
+    __device__ __forceinline__ void store(T *p) const { __builtin_memcpy(p, w, sizeof(w)); }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i >> 2].w[i & 3] = 0;
+        for (unsigned i = 0; i < V * sizeof(T) / 4; ++i) w[i] = 0;
     }
-    __device__ __forceinline__ void get(float (&o)[8]) const {
+    __device__ __forceinline__ void get(float (&o)[V]) const {
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(r[i >> 2].w[i & 3]);
+            for (int i = 0; i < V / 2; ++i) {
+                o[2 * i] = __uint_as_float(w[i] << 16);
+                o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = __uint_as_float(w[i]);
+        }
     }
-    __device__ __forceinline__ void set(const float (&x)[8]) {
+    __device__ __forceinline__ void set(const float (&x)[V]) {
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i >> 2].w[i & 3] = __float_as_uint(x[i]);
+            for (int i = 0; i < V / 2; ++i) w[i] = pack_bf(x[2 * i], x[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(x[i]);
+        }
     }
-    __device__ __forceinline__ void store(float *p) const { __builtin_memcpy(p, r, 32); }
-    __device__ __forceinline__ void part(const float *p, int n) {
-        float v[8];
+    __device__ __forceinline__ void part(const T *p, int n) {  // n < V elements, the others 0
+        T v[V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.f;
-        __builtin_memcpy(r, v, 32);
+        for (int i = 0; i < V; ++i) v[i] = i < n ? p[i] : T(0);
+        __builtin_memcpy(w, v, sizeof(w));
     }
-    __device__ __forceinline__ void store_part(float *p, int n) const {
-        float v[8];
-        __builtin_memcpy(v, r, 32);
+    __device__ __forceinline__ void store_part(T *p, int n) const {
+        T v[V];
+        __builtin_memcpy(v, w, sizeof(w));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < V; ++i)
             if (i < n) p[i] = v[i];
     }
 };
+template <typename T> using Vec8 = Vec<T, 8>;
 
-__host__ __device__ __forceinline__ int vec_count(int D) { return (D + 7) >> 3; }
-// First channel of vector i (D >= 8), or 0 with D < 8, where a vector has D channels.
-__device__ __forceinline__ int vec_channel(int i, int D) {
-    const int c = 8 * i;
-    return D < 8 ? 0 : (c + 8 <= D ? c : D - 8);
+template <int V = 8> __host__ __device__ __forceinline__ int vec_count(int D) { return (D + V - 1) / V; }
+// First channel of vector i (D >= V), or 0 with D < V, where a vector has D channels.
+template <int V = 8> __device__ __forceinline__ int vec_channel(int i, int D) {
+    const int c = V * i;
+    return D < V ? 0 : (c + V <= D ? c : D - V);
 }
-template <typename T> __device__ __forceinline__ void vec_load(Vec8<T> &v, const T *row, int c, int D) {
-    if (D >= 8) v.load(row + c);
+template <typename T, int V> __device__ __forceinline__ void vec_load(Vec<T, V> &v, const T *row, int c, int D) {
+    if (D >= V) v.load(row + c);
     else v.part(row, D);
 }
-template <typename T> __device__ __forceinline__ void vec_store(const Vec8<T> &v, T *row, int c, int D) {
-    if (D >= 8) v.store(row + c);
+template <typename T, int V> __device__ __forceinline__ void vec_store(const Vec<T, V> &v, T *row, int c, int D) {
+    if (D >= V) v.store(row + c);
     else v.store_part(row, D);
 }
 
@@ -103,6 +84,31 @@ __device__ __forceinline__ float load_f32(const void *p, int64_t i, int bf16) {
 // 1 / (1 + e^-x): e^-x overflows to inf for x < -88, whose reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
+}
+
+// Sum of column i over rows [rows][n], by a workgroup of 64 columns by 16 groups of rows: in a fixed
+// order, so results do not depend on scheduling.  The first 64 threads have it.
+__device__ __forceinline__ float sum_rows(const float *rows_of, int rows, int64_t n, int64_t i) {
+    __shared__ float part[16][64];
+    const int g = threadIdx.x >> 6, c = threadIdx.x & 63;
+    float s = 0.f;
+    if (i < n) {
+        int b = g;
+        for (; b + 7 * 16 < rows; b += 8 * 16) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = rows_of[(int64_t)(b + 16 * k) * n + i];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
+        for (; b < rows; b += 16) s += rows_of[(int64_t)b * n + i];
+    }
+    part[g][c] = s;
+    __syncthreads();
+    if (g == 0)
+#pragma unroll
+        for (int k = 1; k < 16; ++k) s += part[k][c];
+    return s;
 }
 
 // Sequence of token t (flattened over the batch), its first token and the token after its
