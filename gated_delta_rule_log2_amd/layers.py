@@ -24,6 +24,9 @@ import torch
 from . import KDAContractError, KDARuntimeError, _abi, _check_tensor, _dtype_code, _ptr, _raise, library
 
 _byref = ctypes.byref
+# the current stream's handle without a Stream object around it (a single token's call is all overhead)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _refuse(code: str, msg: str):
@@ -39,10 +42,10 @@ def _device(t: torch.Tensor, what: str) -> torch.device:
 def _call(fn, dev: torch.device, *args) -> None:
     """fn(*args, stream) with the tensors' device current."""
     if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _raw_stream(dev.index))
     if rc != _abi.KDA_OK:
         _raise(rc, library())
 
@@ -61,15 +64,19 @@ def _scratch(nbytes: int, dev: torch.device) -> torch.Tensor:
     return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
-def _token_stride(t: torch.Tensor, name: str, shape: tuple, dev: torch.device, dtype=None) -> int:
-    """Elements between two tokens of t [B, T, ...]: its inner dimensions are contiguous and
-    its tokens evenly spaced (a slice of a projection's output is)."""
-    if t.shape != torch.Size(shape):
+def _check_place(t: torch.Tensor, name: str, shape: tuple, dev: torch.device, dtype) -> None:
+    if t.shape != shape:
         _refuse("KDA_ERR_SHAPE", f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != dev:
         _refuse("KDA_ERR_SHAPE", f"{name} must be on {dev}")
     if dtype is not None and t.dtype != dtype:
         _refuse("KDA_ERR_DTYPE", f"{name} must be {dtype}")
+
+
+def _token_stride(t: torch.Tensor, name: str, shape: tuple, dev: torch.device, dtype=None) -> int:
+    """Elements between two tokens of t [B, T, ...]: its inner dimensions are contiguous and
+    its tokens evenly spaced (a slice of a projection's output is)."""
+    _check_place(t, name, shape, dev, dtype)
     B, T = shape[:2]
     stride, inner, ok = t.stride(), 1, True
     for i in range(len(shape) - 1, 1, -1):
@@ -80,6 +87,14 @@ def _token_stride(t: torch.Tensor, name: str, shape: tuple, dev: torch.device, d
     if not ok and t.numel() > 0:
         _refuse("KDA_ERR_SHAPE", f"{name} must be contiguous within a token and its tokens evenly spaced")
     return max(step, inner)
+
+
+def _row_stride(t: torch.Tensor, name: str, shape: tuple, dev: torch.device, dtype=None) -> int:
+    """The same of one token for each row, t [rows, ...]."""
+    _check_place(t, name, shape, dev, dtype)
+    if t.is_contiguous():
+        return t.numel() // shape[0]
+    return _token_stride(t.unsqueeze(1), name, (shape[0], 1, *shape[1:]), dev, dtype)
 
 
 class _Offsets:
@@ -109,25 +124,20 @@ def _slots(slots, rows: int, pool: int, dev: torch.device):
 
 
 # ------------------------------------------------------------------------------------- short convolution
-def _conv_desc(x, weight, bias, activation, step, offsets, dy=None):
+def _conv_desc(B, T, x, weight, bias, activation, step, num_seqs, host_ptr, dy=None):
     if activation not in (None, "silu"):
         _refuse("KDA_ERR_UNSUPPORTED", f"activation must be None or 'silu', got {activation!r}")
-    d = _abi.KdaConvDesc()
-    d.B, d.T, d.D = x.shape
-    d.W = weight.shape[1]
-    d.num_seqs, d.cu_seqlens_host = offsets.N, offsets.host_ptr
-    d.x_dtype, d.w_dtype = _dtype_code(x, "x"), _dtype_code(weight, "weight")
-    d.dy_dtype = d.x_dtype if dy is None else _dtype_code(dy, "dy")
-    d.flags = _abi.CONV_SILU if activation else 0
-    d.x_stride = step
-    _check_tensor(weight, "weight", (d.D, d.W), x.device)
-    _check_tensor(bias, "bias", (d.D,), x.device, weight.dtype)
-    return d
+    D, W, dev = x.shape[-1], weight.shape[1], x.device
+    _check_tensor(weight, "weight", (D, W), dev)
+    _check_tensor(bias, "bias", (D,), dev, weight.dtype)
+    code = _dtype_code(x, "x")
+    return _abi.KdaConvDesc(B, T, D, W, num_seqs, host_ptr, code, _dtype_code(weight, "weight"),
+                            code if dy is None else _dtype_code(dy, "dy"), _abi.CONV_SILU if activation else 0, step)
 
 
-def _conv_shapes(x, weight, what):
-    if x.dim() != 3 or weight.dim() != 2 or x.shape[0] < 1:
-        _refuse("KDA_ERR_SHAPE", "x must be [B, T, D] and weight [D, W]")
+def _conv_shapes(x, weight, dims, what):
+    if x.dim() != dims or weight.dim() != 2 or x.shape[0] < 1:
+        _refuse("KDA_ERR_SHAPE", "x must be [B, T, D] (a step [rows, D]) and weight [D, W]")
     if not 2 <= weight.shape[1] <= 4:
         _refuse("KDA_ERR_UNSUPPORTED", f"the convolution's width must be 2, 3 or 4, got {weight.shape[1]}")
     return _device(x, what)
@@ -146,10 +156,10 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     len(cu_seqlens) - 1 with B = 1).  cu_seqlens_host: a CPU copy of cu_seqlens, which spares
     the call the wait for the offsets (needed under graph capture).
     """
-    dev = _conv_shapes(x, weight, "short_conv")
+    dev = _conv_shapes(x, weight, 3, "short_conv")
     B, T, D = x.shape
     offsets = _Offsets(cu_seqlens, cu_seqlens_host, B, dev)
-    d = _conv_desc(x, weight, bias, activation, _token_stride(x, "x", (B, T, D), dev), offsets)
+    d = _conv_desc(B, T, x, weight, bias, activation, _token_stride(x, "x", x.shape, dev), offsets.N, offsets.host_ptr)
     states = (offsets.N, d.W - 1, D)
     _check_tensor(initial_state, "initial_state", states, dev, x.dtype)
     y = torch.empty((B, T, D), dtype=x.dtype, device=dev)
@@ -167,10 +177,10 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, bias
     dtype (dh0 where an initial_state is given), dweight and dbias (with a bias) in float32.
     dy has x's shape, in x's dtype or float32; dht the final state's shape and x's dtype.
     """
-    dev = _conv_shapes(x, weight, "short_conv_bwd")
+    dev = _conv_shapes(x, weight, 3, "short_conv_bwd")
     B, T, D = x.shape
     offsets = _Offsets(cu_seqlens, cu_seqlens_host, B, dev)
-    d = _conv_desc(x, weight, bias, activation, _token_stride(x, "x", (B, T, D), dev), offsets, dy)
+    d = _conv_desc(B, T, x, weight, bias, activation, _token_stride(x, "x", x.shape, dev), offsets.N, offsets.host_ptr, dy)
     states = (offsets.N, d.W - 1, D)
     _check_tensor(dy, "dy", (B, T, D), dev)
     _check_tensor(initial_state, "initial_state", states, dev, x.dtype)
@@ -196,19 +206,17 @@ def short_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, 
     (row b's is b without it).  A slot below 0 or past the pool marks a padding row: y is 0
     there and no state is touched.  Rows must not share a slot.
     """
-    if x.dim() != 2:
-        _refuse("KDA_ERR_SHAPE", "x must be [rows, D]")
-    rows, D = x.shape
-    if rows == 0:
+    if x.dim() == 2 and x.shape[0] == 0:
         return torch.empty_like(x)
-    x3 = x.unsqueeze(1)
-    dev = _conv_shapes(x3, weight, "short_conv_step")
-    d = _conv_desc(x3, weight, bias, activation, _token_stride(x3, "x", (rows, 1, D), dev), _Offsets(None, None, rows, dev))
-    _check_tensor(state, "state", (state.shape[0], d.W - 1, D), dev, x.dtype)
-    _slots(slots, rows, state.shape[0], dev)
+    dev = _conv_shapes(x, weight, 2, "short_conv_step")
+    rows, D = x.shape
+    d = _conv_desc(rows, 1, x, weight, bias, activation, _row_stride(x, "x", x.shape, dev), rows, None)
+    pool = state.shape[0]
+    _check_tensor(state, "state", (pool, d.W - 1, D), dev, x.dtype)
+    _slots(slots, rows, pool, dev)
     y = torch.empty((rows, D), dtype=x.dtype, device=dev)
-    _call(library().kda_short_conv_step, dev, _byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots),
-          state.shape[0], _ptr(y))
+    _call(library().kda_short_conv_step, dev, _byref(d), x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(),
+          _ptr(slots), pool, y.data_ptr())
     return y
 
 
@@ -217,15 +225,11 @@ def _norm_desc(x, weight, eps, group_size, what):
     dev = _device(x, what)
     if x.dim() < 1 or x.shape[-1] < 1:
         _refuse("KDA_ERR_SHAPE", "x must be [..., D]")
-    d = _abi.KdaNormDesc()
-    d.D = x.shape[-1]
-    d.rows = x.numel() // d.D
-    d.group_size = group_size
-    d.x_dtype, d.w_dtype = _dtype_code(x, "x"), _dtype_code(weight, "weight")
-    d.eps = eps
-    _check_tensor(x, "x", x.shape, dev)
-    _check_tensor(weight, "weight", (d.D,), dev)
-    return d, dev
+    D = x.shape[-1]
+    _check_tensor(weight, "weight", (D,), dev)
+    if not x.is_contiguous():
+        _refuse("KDA_ERR_SHAPE", "x must be contiguous")
+    return _abi.KdaNormDesc(x.numel() // D, D, group_size, _dtype_code(x, "x"), _dtype_code(weight, "weight"), eps), dev
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6):
@@ -280,24 +284,21 @@ def rms_norm_bwd(h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, dh: Op
 
 
 # ------------------------------------------------------------------------------- state space scan
-def _ssm_desc(x, dt, A_log, B, C, D, dt_bias, softplus, offsets, what):
-    dev = x.device
-    nb, T, H, P = x.shape
-    d = _abi.KdaSsmDesc()
-    d.B, d.T, d.H, d.P = nb, T, H, P
-    d.G, d.N = B.shape[2:]
-    d.num_seqs, d.cu_seqlens_host = offsets.N, offsets.host_ptr
-    d.x_dtype, d.dt_dtype = _dtype_code(x, "x"), _dtype_code(dt, "dt")
-    d.flags = _abi.SSM_SOFTPLUS if softplus else 0
-    d.x_stride = _token_stride(x, "x", (nb, T, H, P), dev)
-    d.dt_stride = _token_stride(dt, "dt", (nb, T, H), dev)
-    d.b_stride = _token_stride(B, "B", (nb, T, d.G, d.N), dev, x.dtype)
-    d.c_stride = _token_stride(C, "C", (nb, T, d.G, d.N), dev, x.dtype)
+def _ssm_desc(x, dt, A_log, B, C, D, dt_bias, softplus, num_seqs, host_ptr, what):
+    dev, (H, P), (G, N) = x.device, x.shape[-2:], B.shape[-2:]
+    if x.dim() == 4:
+        (nb, T), stride = x.shape[:2], _token_stride
+    else:
+        nb, T, stride = x.shape[0], 1, _row_stride
+    lead = x.shape[:-2]
     if A_log is None:
         _refuse("KDA_ERR_MISSING_A_LOG", f"{what} needs A_log")
     for t, name in ((A_log, "A_log"), (D, "D"), (dt_bias, "dt_bias")):
         _check_tensor(t, name, (H,), dev, torch.float32)
-    return d
+    return _abi.KdaSsmDesc(nb, T, H, G, N, P, num_seqs, host_ptr, _dtype_code(x, "x"), _dtype_code(dt, "dt"),
+                           _abi.SSM_SOFTPLUS if softplus else 0, stride(x, "x", x.shape, dev),
+                           stride(dt, "dt", (*lead, H), dev), stride(B, "B", (*lead, G, N), dev, x.dtype),
+                           stride(C, "C", (*lead, G, N), dev, x.dtype))
 
 
 def _ssm_shapes(x, dt, B, C, dims, what):
@@ -326,7 +327,8 @@ def chunk_ssm(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.T
     """
     dev = _ssm_shapes(x, dt, B, C, 4, "chunk_ssm")
     offsets = _Offsets(cu_seqlens, cu_seqlens_host, x.shape[0], dev)
-    d = _ssm_desc(x, dt, A_log, B, C, D, dt_bias, use_softplus_in_kernel, offsets, "chunk_ssm")
+    d = _ssm_desc(x, dt, A_log, B, C, D, dt_bias, use_softplus_in_kernel, offsets.N, offsets.host_ptr,
+                  "chunk_ssm")
     states = (offsets.N, d.H, d.N, d.P)
     _check_tensor(initial_state, "initial_state", states, dev, torch.float32)
     lib = library()
@@ -349,7 +351,8 @@ def chunk_ssm_bwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: tor
     """
     dev = _ssm_shapes(x, dt, B, C, 4, "chunk_ssm_bwd")
     offsets = _Offsets(cu_seqlens, cu_seqlens_host, x.shape[0], dev)
-    d = _ssm_desc(x, dt, A_log, B, C, D, dt_bias, use_softplus_in_kernel, offsets, "chunk_ssm_bwd")
+    d = _ssm_desc(x, dt, A_log, B, C, D, dt_bias, use_softplus_in_kernel, offsets.N, offsets.host_ptr,
+                  "chunk_ssm_bwd")
     states = (offsets.N, d.H, d.N, d.P)
     _check_tensor(dy, "dy", x.shape, dev, x.dtype)
     _check_tensor(initial_state, "initial_state", states, dev, torch.float32)
@@ -384,11 +387,11 @@ def ssm_step(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Te
         return torch.empty_like(x)
     dev = _ssm_shapes(x, dt, B, C, 3, "ssm_step")
     rows = x.shape[0]
-    d = _ssm_desc(x.unsqueeze(1), dt.unsqueeze(1), A_log, B.unsqueeze(1), C.unsqueeze(1), D, dt_bias,
-                  use_softplus_in_kernel, _Offsets(None, None, rows, dev), "ssm_step")
-    _check_tensor(state, "state", (state.shape[0], d.H, d.N, d.P), dev, torch.float32)
-    _slots(slots, rows, state.shape[0], dev)
+    d = _ssm_desc(x, dt, A_log, B, C, D, dt_bias, use_softplus_in_kernel, rows, None, "ssm_step")
+    pool = state.shape[0]
+    _check_tensor(state, "state", (pool, d.H, d.N, d.P), dev, torch.float32)
+    _slots(slots, rows, pool, dev)
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _call(library().kda_ssm_step, dev, _byref(d), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
-          _ptr(dt_bias), _ptr(state), _ptr(slots), state.shape[0], _ptr(y))
+    _call(library().kda_ssm_step, dev, _byref(d), x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(),
+          _ptr(D), _ptr(dt_bias), state.data_ptr(), _ptr(slots), pool, y.data_ptr())
     return y
