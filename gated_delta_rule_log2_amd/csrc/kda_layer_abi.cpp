@@ -95,8 +95,15 @@ kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {
     return KDA_OK;
 }
 
-// The chunks, and how many of them make a segment: enough segments that the passes over chunks
-// fill the GPU, and at least four chunks in each (joining a segment costs about one).
+// The chunks, and how many of them make a segment.  kCarryGroups segments fill the GPU, and a
+// segment has at least two chunks, since a joined one costs a pass over its state: fp32 gradients of
+// 2 x 1003 tokens, 8 heads of 64 x 64, take 80 us at one, 85 at two, 113 at four chunks.  Where no
+// sequence is longer than 1.5 segments, each is one: states are then not carried over them twice, and
+// the workgroups that end early leave room for others (13 sequences, 64 heads: 176 us against 187 cut
+// at one segment, 163 against 187 for other lengths).
+// dC's and dB's scans sum two heads of a group in a workgroup, which shares the tiles of B and C and
+// halves the parts to be summed (8192 tokens, 32 heads in 16 groups of 128 x 128: 494 us against 614
+// with one head); where that leaves half the CUs without work, one (the fp32 case: 73 us against 85).
 kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p) {
     auto each = [&](auto f) {
         if (d->cu_seqlens_host)
@@ -107,7 +114,9 @@ kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p) {
     each([&](int64_t c, int64_t times) { chunks += c * times; });
     if (chunks * p.H > INT32_MAX) return KDA_ERR_SHAPE;
     const int64_t seg = (chunks * p.H + kCarryGroups - 1) / kCarryGroups;
-    p.seg = (int32_t)(seg < 4 ? 4 : seg);
+    int64_t longest = 0;
+    each([&](int64_t c, int64_t) { longest = c > longest ? c : longest; });
+    p.seg = (int32_t)(seg < 2 ? 2 : 2 * longest <= 3 * seg ? longest : seg);
     each([&](int64_t c, int64_t times) {
         const int64_t s = c > p.seg ? (c + p.seg - 1) / p.seg : 1;
         segs += s * times;
@@ -115,7 +124,8 @@ kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p) {
     });
     if (segs * p.H * 8 > INT32_MAX - 8) return KDA_ERR_SHAPE;
     p.total_chunks = (int32_t)chunks; p.total_segs = (int32_t)segs; p.max_segs = (int32_t)most;
-    p.split = (p.H / p.G + 1) / 2;  // two heads to a workgroup of dC's and dB's scans
+    const int32_t heads = p.H / p.G, pairs = (heads + 1) / 2;
+    p.split = segs * p.G * pairs * ((p.N + 63) / 64) <= kCarryGroups / 2 ? heads : pairs;
     return KDA_OK;
 }
 
