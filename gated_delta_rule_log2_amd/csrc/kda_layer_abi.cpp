@@ -3,8 +3,10 @@
 // checks come before any HIP call, descriptor first, then pointers, then the workspace.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstring>
+#include <functional>
 
 #include "../../include/kda.h"
 #include "kda_layer.h"
@@ -69,7 +71,7 @@ kda_status check_norm(const kda_norm_desc *d, bool fp8, NormParams &p) {
 }
 
 constexpr int64_t kMaxStride = (1 << 24) - 1;  // a chunk's offsets stay in 32 bits
-constexpr int64_t kCarryGroups = 512;  // workgroups wanted of a pass over chunks: two for each CU
+constexpr int64_t kCarryGroups = 512;  // workgroups of a pass over chunks at once: two for each CU
 
 kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {
     if (!d) return KDA_ERR_NULL_POINTER;
@@ -95,31 +97,95 @@ kda_status check_ssm(const kda_ssm_desc *d, SsmParams &p) {
     return KDA_OK;
 }
 
-// The chunks, and how many of them make a segment.  kCarryGroups segments fill the GPU, and a
-// segment has at least two chunks, since a joined one costs a pass over its state: fp32 gradients of
-// 2 x 1003 tokens, 8 heads of 64 x 64, take 80 us at one, 85 at two, 113 at four chunks.  Where no
-// sequence is longer than 1.5 segments, each is one: states are then not carried over them twice, and
-// the workgroups that end early leave room for others (13 sequences, 64 heads: 176 us against 187 cut
-// at one segment, 163 against 187 for other lengths).
+// Time of a pass over segments, in steps of a chunk, on `slots` workgroups at once: items(f) calls
+// f(steps) for each of them, in their order.  A slot costs kItem steps for its states besides; the
+// last ones run faster, with the GPU partly empty.  Few items are dealt out one by one, many fill
+// the slots evenly but for the last.
+constexpr int kDealt = 128;
+template <typename F> double pass_time(F items, int64_t slots) {
+    constexpr double kItem = 1.5, kTail = 0.62;
+    double sum = 0., most = 0.;
+    int64_t count = 0;
+    items([&](int64_t steps) {
+        const double t = (double)steps + kItem;
+        sum += t;
+        if (t > most) most = t;
+        ++count;
+    });
+    const double even = sum / (double)slots;
+    double last = even + 0.5 * most;
+    if (count <= slots) {
+        last = most;
+    } else if (count <= kDealt) {
+        double busy[kDealt], *end = busy + slots;  // a heap, the first slot to be free on top
+        for (double *s = busy; s < end; ++s) *s = 0.;
+        last = 0.;
+        items([&](int64_t steps) {
+            std::pop_heap(busy, end, std::greater<double>());
+            end[-1] += (double)steps + kItem;
+            if (end[-1] > last) last = end[-1];
+            std::push_heap(busy, end, std::greater<double>());
+        });
+    }
+    return last > even ? even + kTail * (last - even) : even;
+}
+
+// The chunks, and how many of them make a segment: the number that takes the least time by the above,
+// of some about the one that gives every slot one segment, and of whole sequences.  Those need no
+// first pass for the segments' states (0.45 of the forward's time for a chunk, which is 1 here) and no
+// joining (2); the backward has both for two directions, and 4.5 of the forward's passes.
+// Measured over 15 packed batches at nine lengths each (8192 or 6000 tokens, 5 to 30 sequences, 32 or
+// 64 heads, forward and backward): 6 % behind the best length on average, where one segment for every
+// slot is 28 % behind.  A segment has at least two chunks: fp32 gradients of 2 x 1003 tokens, 8 heads of
+// 64 x 64, take 80 us at one, 85 at two and 113 at four.
 // dC's and dB's scans sum two heads of a group in a workgroup, which shares the tiles of B and C and
 // halves the parts to be summed (8192 tokens, 32 heads in 16 groups of 128 x 128: 494 us against 614
 // with one head); where that leaves half the CUs without work, one (the fp32 case: 73 us against 85).
-kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p) {
+kda_status plan_ssm(const kda_ssm_desc *d, SsmParams &p, bool backward) {
     auto each = [&](auto f) {
         if (d->cu_seqlens_host)
-            for (int32_t n = 0; n < p.NS; ++n) f((d->cu_seqlens_host[n + 1] - d->cu_seqlens_host[n] + p.L - 1) / p.L, 1);
-        else f((int64_t)(p.T + p.L - 1) / p.L, p.NS);
+            for (int32_t n = 0; n < p.NS; ++n) f((d->cu_seqlens_host[n + 1] - d->cu_seqlens_host[n] + p.L - 1) / p.L);
+        else
+            for (int32_t n = 0; n < p.NS; ++n) f((int64_t)(p.T + p.L - 1) / p.L);
     };
-    int64_t chunks = 0, segs = 0, most = 1;
-    each([&](int64_t c, int64_t times) { chunks += c * times; });
+    int64_t chunks = 0, longest = 1, segs = 0, most = 1;
+    each([&](int64_t c) {
+        chunks += c;
+        if (c > longest) longest = c;
+    });
     if (chunks * p.H > INT32_MAX) return KDA_ERR_SHAPE;
-    const int64_t seg = (chunks * p.H + kCarryGroups - 1) / kCarryGroups;
-    int64_t longest = 0;
-    each([&](int64_t c, int64_t) { longest = c > longest ? c : longest; });
-    p.seg = (int32_t)(seg < 2 ? 2 : 2 * longest <= 3 * seg ? longest : seg);
-    each([&](int64_t c, int64_t times) {
-        const int64_t s = c > p.seg ? (c + p.seg - 1) / p.seg : 1;
-        segs += s * times;
+    const int64_t slots = p.H < kCarryGroups ? (kCarryGroups + p.H / 2) / p.H : 1;
+    auto parts = [](int64_t c, int64_t seg) { return c > seg ? (c + seg - 1) / seg : 1; };
+    double best = 0.;
+    p.seg = (int32_t)longest;
+    for (int k = 0; k <= 6 && longest > 2; ++k) {
+        static const double share[6] = {0.5, 0.75, 1., 1.25, 1.5, 2.};
+        int64_t seg = longest;
+        if (k > 0) {
+            seg = (int64_t)(share[k - 1] * (double)chunks / (double)slots + 0.5);
+            if (seg < 2) seg = 2;
+            if (seg >= longest) break;
+        }
+        auto all = [&](auto f) {
+            each([&](int64_t c) {
+                const int64_t n = parts(c, seg);
+                for (int64_t i = 0; i + 1 < n; ++i) f(seg);
+                f(c - (n - 1) * seg);
+            });
+        };
+        auto first = [&](auto f) {
+            for (int dir = 0; dir < (backward ? 2 : 1); ++dir)
+                each([&](int64_t c) {
+                    for (int64_t i = 1; i < parts(c, seg); ++i) f(seg);
+                });
+        };
+        double t = (backward ? 4.5 : 1.) * pass_time(all, slots);
+        if (seg < longest) t += 0.45 * pass_time(first, slots) + (backward ? 4. : 2.);
+        if (k == 0 || t < best) best = t, p.seg = (int32_t)seg;
+    }
+    each([&](int64_t c) {
+        const int64_t s = parts(c, p.seg);
+        segs += s;
         if (s > most) most = s;
     });
     if (segs * p.H * 8 > INT32_MAX - 8) return KDA_ERR_SHAPE;
@@ -172,14 +238,14 @@ size_t ssm_workspace(SsmParams &p, void *ws, bool backward) {
 
 using namespace kda;
 
-static kda_status ssm_prepare(const kda_ssm_desc *d, SsmParams &p) {
+static kda_status ssm_prepare(const kda_ssm_desc *d, SsmParams &p, bool backward) {
     const kda_status st = check_ssm(d, p);
-    return st == KDA_OK ? plan_ssm(d, p) : st;
+    return st == KDA_OK ? plan_ssm(d, p, backward) : st;
 }
 
 static kda_status ssm_size(const kda_ssm_desc *d, size_t *bytes, bool backward) {
     SsmParams p;
-    const kda_status st = ssm_prepare(d, p);
+    const kda_status st = ssm_prepare(d, p, backward);
     if (st != KDA_OK) return st;
     if (!bytes) return KDA_ERR_NULL_POINTER;
     *bytes = ssm_workspace(p, nullptr, backward);
@@ -295,7 +361,7 @@ kda_status kda_ssm_fwd(const kda_ssm_desc *d, const void *x, const void *dt, con
                        const int64_t *cu_seqlens, void *y, float *final_state, void *workspace,
                        size_t workspace_bytes, hipStream_t stream) {
     SsmParams p;
-    const kda_status st = ssm_prepare(d, p);
+    const kda_status st = ssm_prepare(d, p, false);
     if (st != KDA_OK) return st;
     if (p.tokens > 0 && (!x || !dt || !Bm || !C || !y)) return KDA_ERR_NULL_POINTER;
     if (!A_log) return KDA_ERR_MISSING_A_LOG;
@@ -313,7 +379,7 @@ kda_status kda_ssm_bwd(const kda_ssm_desc *d, const void *x, const void *dt, con
                        float *dA_log, void *dB, void *dC, float *dD, float *ddt_bias, float *dh0, void *workspace,
                        size_t workspace_bytes, hipStream_t stream) {
     SsmParams p;
-    const kda_status st = ssm_prepare(d, p);
+    const kda_status st = ssm_prepare(d, p, true);
     if (st != KDA_OK) return st;
     if (p.tokens > 0 && (!x || !dt || !Bm || !C || !dy || !dx || !ddt || !dB || !dC)) return KDA_ERR_NULL_POINTER;
     if (!dA_log) return KDA_ERR_NULL_POINTER;
