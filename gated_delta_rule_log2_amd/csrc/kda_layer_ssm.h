@@ -364,7 +364,8 @@ template <typename T, int KW, int CT, int MODE> struct ScanLds {
     static constexpr int L = ChunkLen<T>::value, VW = 64 * CT;
     T key[L * Layout<T, KW>::LD], val[L * Layout<T, VW>::LD];
     T q[MODE == kFirst ? 4 : L * Layout<T, KW>::LD];
-    T m[MODE == kFirst ? 4 : L * Layout<T, 64>::LD];
+    static constexpr int MPARTS = sizeof(T) == 2 && scan_sums(MODE) ? 2 : 1, MSIZE = L * Layout<T, 64>::LD;
+    T m[MODE == kFirst ? 4 : MPARTS * MSIZE];
     T other[MODE == kDx || scan_sums(MODE) ? L * Layout<T, VW>::LD : 4];  // x; or C, B for dC, dB
     float tok[5][L];
     float rows[MODE == kDx ? 4 : 1][L], cols[MODE == kDx ? 4 : 1][L], diag[L], qdiag[L];
@@ -379,11 +380,13 @@ template <typename T, int KW, int CT, int MODE> struct ScanLds {
 //   - out = M v + factor Z^T q, with v^T and Z^T as the left operands: a lane ends with consecutive
 //     columns of one token, and the accumulators that hold Z are, in pairs, its fragments;
 //   - Z' = decay Z + k^T (factor v).
-// M and (for y and dx) Z are rounded to the input's type for their products, as y and dx are at
+// For y and dx, M and Z are rounded to the input's type for their products, as y and dx are at
 // their store.  Z itself is carried in fp32 and its scaled v goes through the products in three
 // bf16 parts, so that it is as exact as an fp32 sum; so does Z for dC and dB, whose dot products
-// with C and B (w_o, w_q) are parts of the decays' gradients and leave in fp32.  The next chunk's
-// tiles are requested before this one's products.
+// with C and B (w_o, w_q) are parts of the decays' gradients and leave in fp32.  M has two parts
+// there: with one, sums over a group's few heads were off by 1.4 to 1.55 of their final rounding
+// (two cost 504 us against 491 in the gradients of 8192 tokens, 32 heads).  The next chunk's tiles
+// are requested before this one's products.
 // kFirst: the states of segments from zero to seg_state (all but a sequence's last segment), the
 // scan of dC or, in the second half of the grid, of dB, without outputs.
 // kDx also leaves, per chunk and head, the sums over W_ba = (C_b . B_a) e^{cum_b - cum_a} (dy_b . x_a),
@@ -574,7 +577,14 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
                             if (g == 0) lds.cols[jt][a] = cols;
                         }
                     }
-                    store_run(lds.m + Layout<T, 64>::at(a, b0), {acc[0], acc[1], acc[2], acc[3]});
+                    const float m[4] = {acc[0], acc[1], acc[2], acc[3]};
+                    store_run(lds.m + Layout<T, 64>::at(a, b0), m);
+                    if constexpr (M::MPARTS == 2) {
+                        float hi[4];
+                        const uint32_t u[2] = {pack_bf(m[0], m[1]), pack_bf(m[2], m[3])};
+                        load_run(reinterpret_cast<const uint16_t *>(u), hi);
+                        store_run(lds.m + M::MSIZE + Layout<T, 64>::at(a, b0), {m[0] - hi[0], m[1] - hi[1], m[2] - hi[2], m[3] - hi[3]});
+                    }
                     phase();
                 }
                 if constexpr (MODE == kDx) {
@@ -634,9 +644,12 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
                         for (int ct = 0; ct < CT; ++ct) mv[ct] = zero4();
 #pragma unroll
                         for (int kb = REV ? it / 2 : 0; kb < (REV ? KS : it / 2 + 1); ++kb) {
-                            const Frag<T> fm = row_frag<true, 64>(lds.m, i, 32 * kb, g);
 #pragma unroll
-                            for (int ct = 0; ct < CT; ++ct) mv[ct] = mma(mv[ct], fv[kb][ct], fm);
+                            for (int s = 0; s < M::MPARTS; ++s) {
+                                const Frag<T> fm = row_frag<true, 64>(lds.m + s * M::MSIZE, i, 32 * kb, g);
+#pragma unroll
+                                for (int ct = 0; ct < CT; ++ct) mv[ct] = mma(mv[ct], fv[kb][ct], fm);
+                            }
                         }
                         const float f = lds.tok[4][i], scale = REV ? lds.tok[0][i] : 1.f;
                         const bool real = i < len;

@@ -505,9 +505,11 @@ kda_status kda_rms_norm_bwd(const kda_norm_desc *d, const void *h, const void *w
  *   x_stride, dt_stride, b_stride, c_stride   elements between two tokens (at least H * P, H,
  *                G * N, G * N); y and every gradient are contiguous
  *   flags        KDA_SSM_SOFTPLUS
+ * KDA_ERR_SHAPE also where H * P, G * N or a stride of x, B or C is above 2^24 - 1, B * T above
+ * 2^30 - 1, or the chunks times H (segments times 8 H) above 2^31 - 1.
  * A token's decay below 2^-200 is taken as that (0 in fp32).  A NaN or infinity in a token
- * reaches the later tokens of its sequence, and may reach earlier ones of its chunk; it never
- * reaches another sequence.
+ * reaches the later tokens of its sequence, and may reach earlier ones of its chunk (an infinity as
+ * NaN); it never reaches another sequence.
  */
 enum { KDA_SSM_SOFTPLUS = 1u << 0 };
 typedef struct kda_ssm_desc {
