@@ -47,20 +47,23 @@ __device__ __forceinline__ f32x4 mma(f32x4 acc, const Frag<float> &a, const Frag
 }
 
 // A tile [rows][W] in LDS (W = 64 or 128).  Two-byte rows fill the 64 banks once (W = 128) or
-// half; their 16-byte units are permuted by a function of the row, so that 16 rows read at one
-// column (rows as fragments) and eight rows read over two units (columns as fragments, the
-// transposing read) meet every bank once.  fp32 rows are padded by four.
+// half; their 16-byte units are permuted by a function of the row.  The banks serve 32 lanes of an
+// 8-byte read at a time, and 16 of a 16-byte read, which are not neighbours: lanes 0-3, 12-15 and
+// 20-27, or 4-11, 16-19 and 28-31.  So the function has 16 values over 16 rows, those of rows 0-3 and
+// 12-15 in pairs that differ in the last bit (fragments of rows, where lanes 16-31 read the next
+// unit), and eight neighbouring rows have it differ above that bit (fragments of columns, over two
+// units).  fp32 rows are padded by four.
 template <typename T, int W> struct Layout;
 template <> struct Layout<uint16_t, 128> {
     static constexpr int LD = 128;
     static __device__ __forceinline__ int at(int row, int col) {
-        return row * 128 + (col ^ ((((row & 7) << 1) | ((row >> 3) & 1)) << 3));
+        return row * 128 + (col ^ ((((row & 7) << 1 | (row >> 3 & 1)) ^ (row & 8)) << 3));
     }
 };
 template <> struct Layout<uint16_t, 64> {
     static constexpr int LD = 64;
     static __device__ __forceinline__ int at(int row, int col) {
-        return row * 64 + (col ^ (((((row >> 1) & 3) << 1) | ((row >> 3) & 1)) << 3));
+        return row * 64 + (col ^ ((((row >> 1 & 3) << 1 | (row >> 3 & 1)) ^ (row >> 1 & 4)) << 3));
     }
 };
 template <int W> struct Layout<float, W> {
@@ -68,13 +71,20 @@ template <int W> struct Layout<float, W> {
     static __device__ __forceinline__ int at(int row, int col) { return row * LD + col; }
 };
 
+// Eight bytes of LDS by a read of its own: volatile, because two reads at one distance merge into one
+// of twice the size, whose 16 lanes at a time then meet in their banks (gradients of 8192 tokens, 32
+// heads: 497 us against 512, and half as many LDS cycles; packed forward 152 against 157).
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x2 read_one(const uint16_t *p) {
+    return *(const volatile __attribute__((address_space(3))) u32x2 *)(p);
+}
+
 // Row `row`'s elements k0 .. k0 + 31 of the contraction.
 template <bool PERM, int W> __device__ __forceinline__ Frag<uint16_t> row_frag(const uint16_t *tile, int row, int k0, int g) {
     using Y = Layout<uint16_t, W>;
     Frag<uint16_t> f;
     if constexpr (PERM) {
-        const uint2 a = *reinterpret_cast<const uint2 *>(tile + Y::at(row, k0 + 4 * g));
-        const uint2 b = *reinterpret_cast<const uint2 *>(tile + Y::at(row, k0 + 16 + 4 * g));
+        const u32x2 a = read_one(tile + Y::at(row, k0 + 4 * g)), b = read_one(tile + Y::at(row, k0 + 16 + 4 * g));
         f.u = make_uint4(a.x, a.y, b.x, b.y);
     } else {
         f.u = *reinterpret_cast<const uint4 *>(tile + Y::at(row, k0 + 8 * g));
