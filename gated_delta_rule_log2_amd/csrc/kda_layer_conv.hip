@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvParams p, Lanes 
                     for (int j = 0; j < V; ++j) pre[j] *= sigmoid(pre[j]);
                 Vec<T, V> o;
                 o.set(pre);
-                vec_store(o, y + t * p.D, c, p.D);
+                vec_store_stream(o, y + t * p.D, c, p.D);
                 ++t;
             }
         }

@@ -21,6 +21,24 @@ template <typename T, int V> struct Vec {
     uint32_t w[V * sizeof(T) / 4];
     __device__ __forceinline__ void load(const T *p) { __builtin_memcpy(w, p, sizeof(w)); }
     __device__ __forceinline__ void store(T *p) const { __builtin_memcpy(p, w, sizeof(w)); }
+    // Past the caches: for inputs that nothing reads again, and outputs that only a later kernel reads
+    // (there the read costs what the store saved, no more).  Vectors of one access only: those of two
+    // (fp32, V = 8) fetch their lines twice.
+    typedef uint32_t Raw __attribute__((ext_vector_type(V * sizeof(T) / 4), aligned(sizeof(T))));
+    __device__ __forceinline__ void load_stream(const T *p) {
+        if constexpr (sizeof(w) <= 16) {
+            const Raw r = __builtin_nontemporal_load(reinterpret_cast<const Raw *>(p));
+            __builtin_memcpy(w, &r, sizeof(w));
+        } else {
+            load(p);
+        }
+    }
+    __device__ __forceinline__ void store_stream(T *p) const {
+        static_assert(sizeof(w) <= 16, "a vector of one access");
+        Raw r;
+        __builtin_memcpy(&r, w, sizeof(w));
+        __builtin_nontemporal_store(r, reinterpret_cast<Raw *>(p));
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (unsigned i = 0; i < V * sizeof(T) / 4; ++i) w[i] = 0;
@@ -74,6 +92,14 @@ template <typename T, int V> __device__ __forceinline__ void vec_load(Vec<T, V> 
 }
 template <typename T, int V> __device__ __forceinline__ void vec_store(const Vec<T, V> &v, T *row, int c, int D) {
     if (D >= V) v.store(row + c);
+    else v.store_part(row, D);
+}
+template <typename T, int V> __device__ __forceinline__ void vec_load_stream(Vec<T, V> &v, const T *row, int c, int D) {
+    if (D >= V) v.load_stream(row + c);
+    else v.part(row, D);
+}
+template <typename T, int V> __device__ __forceinline__ void vec_store_stream(const Vec<T, V> &v, T *row, int c, int D) {
+    if (D >= V) v.store_stream(row + c);
     else v.store_part(row, D);
 }
 

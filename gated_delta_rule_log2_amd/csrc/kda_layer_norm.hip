@@ -215,9 +215,9 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 3) norm
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = r + k * TPR < nv ? r + k * TPR : nv - 1, c = vec_channel(i, p.D);
-            vec_load(vh[k], static_cast<const T *>(p.x) + row * p.D, c, p.D);
-            vec_load(vd[k], static_cast<const T *>(p.dy) + row * p.D, c, p.D);
-            vec_load(ve[k], static_cast<const T *>(p.dh ? p.dh : p.x) + row * p.D, c, p.D);
+            vec_load_stream(vh[k], static_cast<const T *>(p.x) + row * p.D, c, p.D);
+            vec_load_stream(vd[k], static_cast<const T *>(p.dy) + row * p.D, c, p.D);
+            vec_load_stream(ve[k], static_cast<const T *>(p.dh ? p.dh : p.x) + row * p.D, c, p.D);
         }
     };
     if (AHEAD && (int64_t)blockIdx.x < steps) request(blockIdx.x);
