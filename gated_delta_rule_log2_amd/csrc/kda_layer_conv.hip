@@ -7,9 +7,11 @@
 // inputs before it, oldest first) or 0.  Sums in fp32 from the stored values, one rounding
 // at the store.
 //
-// Bound by HBM: 2 W + 5 operations for each input read and output written (8192 tokens of 4096
-// channels in bf16: 134 MB in 42 us, 3.2 TB/s; backward 201 MB in 59 us, 3.4 TB/s).  A thread
-// owns four channels and a run of tokens, and keeps the window of W inputs in registers, so x
+// Forward bound by HBM: 2 W + 5 operations for each input read and output written (8192 tokens of 4096
+// channels in bf16: 134 MB in 33 us, 4.1 TB/s).  Backward as much by its arithmetic, 32 vector
+// instructions for each value of x and dy (the same size: 201 MB in 58 us, of which the vector units are
+// busy for half; runs of 32 or 48 tokens, and uniform tokens and addresses in a wave, took as long).  A
+// thread owns four channels and a run of tokens, and keeps the window of W inputs in registers, so x
 // is read once but for the W - 1 tokens before each run, which the neighbouring run has just
 // brought into L2.
 #include "kda_layer.h"
@@ -43,10 +45,11 @@ template <int W, int V> struct Weights {
     }
 };
 
-// Tokens of a batch: a multiple of W, for the turning windows.
 // Channels of a thread: with eight, whose windows and weights leave three waves to a SIMD forward and
-// one backward, 8192 tokens of 4096 channels took 48 and 92 us, with four 42 and 59.
+// one backward, 8192 tokens of 4096 channels took 48 and 92 us, with four 42 and 59 (then streaming
+// stores brought the forward to 33).
 constexpr int kFwdV = 4, kBwdV = 4;
+// Tokens of a batch: a multiple of W, for the turning windows.
 template <int W> struct Batch { static constexpr int value = W == 3 ? 3 : 4; };
 
 // Input at place `pos` of sequence n (first token s0): a token, an initial state's row
@@ -357,7 +360,8 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvParams p) {
 
 // Tokens of one thread: longer runs repeat fewer window loads and leave fewer partial sums, shorter
 // ones fill the chip where there are few vectors.  At 8192 tokens of 4096 channels in bf16 runs of 32
-// took 42 us forward and 64 took 59 us backward; 16 took 47 and 72, and 128 backward 81.
+// took 42 us forward (33 with streaming stores, where 64 took 37) and 64 took 59 us backward; 16 took
+// 47 and 72, and 128 backward 81.
 int run_of(const ConvParams &p) {
     const int64_t vectors = vec_count<kFwdV>(p.D) * p.tokens;
     return vectors >= ((int64_t)1 << 22) ? 32 : vectors >= ((int64_t)1 << 20) ? 8 : 4;
