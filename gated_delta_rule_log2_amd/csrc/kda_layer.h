@@ -52,7 +52,7 @@ struct SsmParams {
     int32_t L, total_chunks, seg, total_segs, max_segs;  // max_segs: of one sequence
     int32_t x_bf16, dt_bf16, softplus;
     int32_t num_slots;
-    int32_t split;                 // backward: parts of a group's heads (two to a part), each with its own sums for dB, dC
+    int32_t split;                 // backward: parts of a group's heads (one or two to a part), each with its own sums for dB, dC
     int64_t tokens;                // B * T
     int64_t x_stride, dt_stride, b_stride, c_stride;
     const void *x, *dt, *Bm, *C, *dy;

@@ -397,6 +397,12 @@ template <typename T, int KW, int CT, int MODE> struct ScanLds {
 // there: with one, sums over a group's few heads were off by 1.4 to 1.55 of their final rounding
 // (two cost 504 us against 491 in the gradients of 8192 tokens, 32 heads).  The next chunk's tiles
 // are requested before this one's products.
+// Bound, at 8192 tokens and 32 heads of 128 x 128 in bf16 (512 workgroups, two for each CU by their
+// registers, 4.6 TB/s and less): no unit alone.  y takes 75 us, the states before it 43; dx 101, dC and
+// dB 150 each, the states of both directions 80.  Of the states' pass the matrix units are busy for 31 %
+// and the vector units for 40 %, of dC's for 19 and 43 % with LDS at 23 %; the rest is waiting at the three
+// barriers of a step and for operands, with two waves to a SIMD.  More waves with smaller tiles (16
+// columns to a wave, three or four workgroups) took as long: they form q k^T twice.
 // kFirst: the states of segments from zero to seg_state (all but a sequence's last segment), the
 // scan of dC or, in the second half of the grid, of dB, without outputs.
 // kDx also leaves, per chunk and head, the sums over W_ba = (C_b . B_a) e^{cum_b - cum_a} (dy_b . x_a),
