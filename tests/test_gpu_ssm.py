@@ -48,6 +48,10 @@ CASES = {
     "packed": ("bf16", 1, 420, 4, 2, 64, 64, [0, 0, 1, 64, 129, 130, 420, 420], True, True, 0),
     "packed in 32 bits": ("fp32", 1, 230, 2, 1, 64, 96, [0, 200, 200, 231 - 1], True, True, 0),
     "packed without states": ("bf16", 1, 300, 2, 1, 32, 64, [0, 290, 300], True, False, 0),
+    # batches that fill the GPU uncut, a segment to a sequence of several chunks
+    "whole sequences": ("bf16", 40, 200, 16, 4, 32, 32, None, True, True, 0),
+    "whole sequences in 32 bits": ("fp32", 24, 100, 32, 8, 32, 32, None, True, True, 0),
+    "one long sequence among short ones": ("bf16", 1, 2260, 32, 8, 32, 64, [0, *range(700, 2261, 130)], True, True, 0),
     "all empty": ("bf16", 1, 0, 2, 1, 32, 32, [0, 0, 0], True, True, 0),
 }
 
