@@ -10,7 +10,10 @@
 // (no difference of large sums in the last), ddt_bias = sum ddt, dD = sum dy . x.  Across chunks
 //   K = <R, S0'> - sum q,   <R, S0'> of the chunk before = K + sum o,
 // from the product <R, S> behind the segment that the scan of dB formed (S0' the state behind the
-// chunk).
+// chunk).  Each step of this chain adds the sums' fp32 rounding, which reaches all of a chunk's steps.
+// Where the chain ends at a known value (the product behind the segment before, 0 in front of a
+// sequence without an initial state, K = 0 of a chunk that forgets its start), what it is off by
+// there is taken back in proportion to the steps.
 #include "kda_layer_ssm.h"
 
 namespace kda {
@@ -44,6 +47,11 @@ __global__ void __launch_bounds__(64 * kStepWaves) ssm_step_grad_kernel(SsmParam
     const int tiles = p.N / 16, L = p.L;
     double behind = 0.;  // <R, S0'> behind the last chunk not yet done
     for (int k = 0; k < tiles; ++k) behind += p.w_dot[((size_t)seg * p.H + h) * tiles + k];
+    // <R, S> in front of the segment, where it is known
+    const bool inner = sg.rank + 1 < sg.segs, anchored = inner || !p.h0;
+    double before = 0.;
+    if (inner)
+        for (int k = 0; k < tiles; ++k) before += p.w_dot[((size_t)(seg - 1) * p.H + h) * tiles + k];
     const float A = -expf(p.A_log[h]);
     for (int k0 = 0; k0 < sg.count; k0 += kStepWaves) {
         const bool mine = k0 + w < sg.count;
@@ -78,12 +86,23 @@ __global__ void __launch_bounds__(64 * kStepWaves) ssm_step_grad_kernel(SsmParam
             forgets[w] = lh + ll < -24.f;
         }
         __syncthreads();
+        // the chain over this round's chunks; own: K of this wave's, and the chunk after the last known place
         double K = 0.;
-        for (int k = 0; k < kStepWaves && k0 + k < sg.count; ++k) {
-            const double through = forgets[k] ? 0. : behind - q_sum[k];
-            if (k == w) K = through;
+        int from = 0, own_from = 0;
+        bool open = false;
+        const int m = sg.count - k0 < kStepWaves ? sg.count - k0 : kStepWaves;
+        for (int k = 0; k < m; ++k) {
+            double through = behind - q_sum[k];
+            if (forgets[k]) {
+                if (open) K -= through * (2 * (w - own_from) + 1) / (2 * (k - own_from) + 1);
+                open = false;
+                through = 0.;
+                from = k + 1;
+            }
+            if (k == w) K = through, own_from = from, open = !forgets[k];
             behind = through + o_sum[k];
         }
+        if (open && anchored && k0 + m == sg.count) K += (before - behind) * (2 * (w - own_from) + 1) / (2 * (m - own_from));
         const double dl = suffix_sum((double)(rows + o) - (double)(d * cols), lane) + (q_all - q_from) + K;
         const float dd = (float)(A * dl) + (cols + diag + qd);
         const float raw = p.softplus ? -dd * expm1f(-d) : dd;  // sigmoid(dt) = 1 - e^-softplus(dt)
