@@ -67,7 +67,7 @@ struct SsmParams {
     float *seg_dec;                // [2][total_segs][H]
     // backward, for the gradients of steps and decays (kda_layer_ssm_bwd.hip)
     float *last_state;             // [NS][H][N][P]
-    float *w_rows, *w_cols, *w_diag, *w_qdiag, *w_decay;  // [total_chunks][H][L], w_decay without [L]
+    float *w_dl, *w_cols, *w_diag, *w_qdiag, *w_decay;  // [total_chunks][H][L], w_decay without [L]
     float *w_o, *w_q;              // [total_chunks][H][N / 16][L]
     float *w_dot;                  // [total_segs][H][N / 16]
     float *sums;                   // [total_chunks][H][4] terms of dA_log, ddt_bias, dD

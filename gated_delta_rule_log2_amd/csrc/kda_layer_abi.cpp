@@ -216,7 +216,7 @@ size_t ssm_workspace(SsmParams &p, void *ws, bool backward) {
     }
     if (backward) {
         p.last_state = floats((size_t)p.NS * p.H * state);
-        p.w_rows = floats(ch * p.L);
+        p.w_dl = floats(ch * p.L);
         p.w_cols = floats(ch * p.L);
         p.w_diag = floats(ch * p.L);
         p.w_qdiag = floats(ch * p.L);

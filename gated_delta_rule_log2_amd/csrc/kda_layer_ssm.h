@@ -365,6 +365,21 @@ __device__ __forceinline__ int fresh(int v) {
 // that registers spill, and a spill's reload waits for every tile load issued before it.
 __device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
+// Sum over this lane and the later ones of its 16, and the value of a row's first lane.
+template <int N> __device__ __forceinline__ float row_shl(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x100 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float row_suffix16(float x) {
+    x += row_shl<1>(x);
+    x += row_shl<2>(x);
+    x += row_shl<4>(x);
+    x += row_shl<8>(x);
+    return x;
+}
+template <int ROW> __device__ __forceinline__ float row_first(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 16 * ROW));
+}
+
 enum ScanMode { kFirst, kY, kDx, kDc, kDb };
 
 constexpr bool scan_sums(int mode) { return mode == kDc || mode == kDb; }  // outputs summed over a group's heads
@@ -406,7 +421,7 @@ template <typename T, int KW, int CT, int MODE> struct ScanLds {
 // kFirst: the states of segments from zero to seg_state (all but a sequence's last segment), the
 // scan of dC or, in the second half of the grid, of dB, without outputs.
 // kDx also leaves, per chunk and head, the sums over W_ba = (C_b . B_a) e^{cum_b - cum_a} (dy_b . x_a),
-// b > a: over a with d_a (w_rows), over b (w_cols), over both with d_a (cum_b - cum_a) in log2
+// b > a: for each t over a < t <= b with d_a (w_dl), over b (w_cols), over both with d_a (cum_b - cum_a) in log2
 // (w_decay), and its diagonal without and with only dy . x (w_diag, w_qdiag).
 template <typename T, int KW, int CT, int MODE>
 __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slices, int dirs) {
@@ -610,10 +625,23 @@ __global__ void __launch_bounds__(256, 2) ssm_scan_kernel(SsmParams p, int slice
                 }
                 __syncthreads();
                 if (MODE == kDx && tid < L) {
-                    float rows = 0.f, cols = 0.f;
-                    for (int t = 0; t <= tid / 16; ++t) rows += lds.rows[t][tid];
-                    for (int t = tid / 16; t < IT; ++t) cols += lds.cols[t][tid];
-                    *behind(p.w_rows + chn * L, tid) = rows;
+                    // the sum over a < t <= b for this thread's t, by blocks: sums of whole ones, of rows from t
+                    // and columns before t of those in t's block row or column, and of its diagonal one, alone
+                    // a difference (of rows and columns from t on)
+                    const int own = tid / 16;
+                    const float d = lds.tok[0][tid], own_col = lds.cols[own][tid];
+                    float rows = lds.rows[own][tid] - d * own_col, far = 0.f;
+                    for (int t = 0; t < own; ++t) rows += lds.rows[t][tid];
+                    for (int t = own + 1; t < IT; ++t) far += lds.cols[t][tid];
+                    const float cols = own_col + far;
+                    float dl = row_suffix16(rows) + row_scan16(row_shr<1>(d * far));
+                    if constexpr (IT == 4) {
+                        const float r0 = row_suffix16(lds.rows[0][tid]), r1 = row_suffix16(lds.rows[1][tid]);
+                        // read where every lane takes part: under the choice the sums would be formed by its lanes alone
+                        const float b20 = row_first<2>(r0), b30 = row_first<3>(r0), b31 = row_first<3>(r1);
+                        dl += own == 1 ? b20 + b30 : own == 2 ? b30 + b31 : 0.f;
+                    }
+                    *behind(p.w_dl + chn * L, tid) = dl;
                     *behind(p.w_cols + chn * L, tid) = cols;
                     *behind(p.w_diag + chn * L, tid) = lds.diag[tid];
                     *behind(p.w_qdiag + chn * L, tid) = lds.qdiag[tid];

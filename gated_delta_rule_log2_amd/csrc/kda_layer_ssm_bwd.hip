@@ -4,7 +4,7 @@
 // A decay e^{d_t A} lies between tokens a < t <= b.  Inside a chunk, with the scans' terms
 //   W_ba = (C_b . B_a) e^{cum_b - cum_a} (dy_b . x_a) (a < b),   o_b = e^{cum_b} C_b . S0 dy_b,
 //   q_a = d_a e^{cum_L - cum_a} B_a . R x_a,   K = e^{cum_L} <R, S0>  (R behind the chunk):
-//   dl_t = sum_{b >= t} (sum_a d_a W_ba + o_b) - sum_{a >= t} d_a sum_b W_ba + sum_{a < t} q_a + K
+//   dl_t = sum_{a < t <= b} d_a W_ba + sum_{b >= t} o_b + sum_{a < t} q_a + K
 //   dd_t = A dl_t + sum_b W_bt + (C_t . B_t) (dy_t . x_t) + q_t / d_t      (formed without dividing)
 //   dA_log = sum W_ba d_a (cum_b - cum_a) + sum o_b cum_b + sum q_a (cum_L - cum_a) + K cum_L
 // (no difference of large sums in the last), ddt_bias = sum ddt, dD = sum dy . x.  Across chunks
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(64 * kStepWaves) ssm_step_grad_kernel(SsmParam
         const int token = sg.token + (c - sg.first) * L, len = sg.end - token < L ? sg.end - token : L;
         const bool in = lane < L;
         const size_t at = chn * L + (in ? lane : 0);
-        float rows = p.w_rows[at], cols = p.w_cols[at], diag = p.w_diag[at], dyx = p.w_qdiag[at];
+        float inner_dl = p.w_dl[at], cols = p.w_cols[at], diag = p.w_diag[at], dyx = p.w_qdiag[at];
         const float d = p.d[at], ch = p.ch[at], cl = p.cl[at], lh = p.ch[chn * L + L - 1], ll = p.cl[chn * L + L - 1];
         float o = 0.f, qd = 0.f;
         float os[8], qs[8];  // of at most eight tiles, all requested at once
@@ -74,10 +74,10 @@ __global__ void __launch_bounds__(64 * kStepWaves) ssm_step_grad_kernel(SsmParam
         for (int k = 0; k < 8; ++k)
             if (k < tiles) o += os[k], qd += qs[k];
         const bool real = lane < len;
-        if (!real) rows = cols = diag = dyx = o = qd = 0.f;
+        if (!real) inner_dl = cols = diag = dyx = o = qd = 0.f;
         const float q = d * qd;
         const double q_from = suffix_sum(q, lane), q_all = __shfl(q_from, 0, 64);
-        const double o_all = __shfl(suffix_sum(o, lane), 0, 64);
+        const double o_from = suffix_sum(o, lane), o_all = __shfl(o_from, 0, 64);
         // K is a difference, off by some 1e-7 of the sums; where the chunk's whole decay is below
         // fp32's rounding it is 0 to that precision, and the sums' errors end there too
         if (lane == 0) {
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(64 * kStepWaves) ssm_step_grad_kernel(SsmParam
             behind = through + o_sum[k];
         }
         if (open && anchored && k0 + m == sg.count) K += (before - behind) * (2 * (w - own_from) + 1) / (2 * (m - own_from));
-        const double dl = suffix_sum((double)(rows + o) - (double)(d * cols), lane) + (q_all - q_from) + K;
+        const double dl = (double)inner_dl + o_from + (q_all - q_from) + K;
         const float dd = (float)(A * dl) + (cols + diag + qd);
         const float raw = p.softplus ? -dd * expm1f(-d) : dd;  // sigmoid(dt) = 1 - e^-softplus(dt)
         constexpr float kLn2 = 0.6931471805599453f;
