@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(64 * kStepWaves) ssm_step_grad_kernel(SsmParam
             forgets[w] = lh + ll < -24.f;
         }
         __syncthreads();
-        // the chain over this round's chunks; own: K of this wave's, and the chunk after the last known place
+        // the chain over these chunks; own: K of this wave's, and the chunk after the last known place
         double K = 0.;
         int from = 0, own_from = 0;
         bool open = false;
