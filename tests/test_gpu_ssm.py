@@ -52,6 +52,7 @@ CASES = {
     "whole sequences": ("bf16", 40, 200, 16, 4, 32, 32, None, True, True, 0),
     "whole sequences in 32 bits": ("fp32", 24, 100, 32, 8, 32, 32, None, True, True, 0),
     "one long sequence among short ones": ("bf16", 1, 2260, 32, 8, 32, 64, [0, *range(700, 2261, 130)], True, True, 0),
+    "pairs of heads in 32 bits": ("fp32", 2, 100, 4, 1, 128, 64, None, True, True, 0),
     "all empty": ("bf16", 1, 0, 2, 1, 32, 32, [0, 0, 0], True, True, 0),
 }
 
@@ -305,10 +306,12 @@ def test_steps_continue_a_prompt():
 
 
 @pytest.mark.gpu
-def test_captured_and_replayed():
-    a, grads, cu, softplus, _ = make("packed", 8)
+@pytest.mark.parametrize("case", ["packed", "a chunk and one"])
+def test_captured_and_replayed(case):
+    a, grads, cu, softplus, _ = make(case, 8)
     d = {k: on_gpu(v) for k, v in a.items()}
-    dy, dht, cu_dev, state = grads["dy"].to(DEV), grads["dht"].to(DEV), cu.to(DEV), d["h0"].clone()
+    dy, dht, state = grads["dy"].to(DEV), grads["dht"].to(DEV), d["h0"].clone()
+    cu_dev = None if cu is None else cu.to(DEV)
 
     def everything():
         y, ht = kda.chunk_ssm(d["x"], d["dt"], d["A_log"], d["B"], d["C"], d["D"], d["dt_bias"], softplus, d["h0"], True, cu_dev,
