@@ -9,8 +9,9 @@
 //
 // Bound by HBM: each value is read once and written once per output, with about ten
 // operations (8192 rows of 4096 in bf16: to 8 bits 236 MB in 52 us, 4.5 TB/s; backward 268 MB
-// in 51 us, 5.3 TB/s, where loads that stay in the caches took 71).  A row stays in the registers of one wave (D <= 1024) or one workgroup between
-// the sum of squares and the output; sums are fp32.
+// in 51 us, 5.3 TB/s, where loads that stay in the caches took 71).  A row stays in the
+// registers of one wave (D <= 1024) or one workgroup between the sum of squares and the output;
+// sums are fp32.
 #include "kda_layer.h"
 #include "kda_layer_device.h"
 
